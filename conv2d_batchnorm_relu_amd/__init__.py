@@ -19,9 +19,16 @@ import os
 __all__ = ["CbrError", "CbrShape", "make_shape", "cbr_status_str", "cbr_output_hw", "cbr_mask_words",
            "cbr_workspace_bytes", "cbr_forward_train", "cbr_forward_infer", "cbr_backward",
            "cbr_conv2d_bias_relu", "cbr_conv2d_bias", "cbr_forward_train_noalloc",
-           "CBR_OP_TRAIN", "CBR_OP_INFER", "CBR_OP_BWD", "library_path"]
+           "CBR_OP_TRAIN", "CBR_OP_INFER", "CBR_OP_BWD", "library_path",
+           "CbrBlockShape", "make_block_shape", "cbr_block_norm_workspace_bytes", "cbr_block_norm_forward",
+           "cbr_block_norm_backward", "CbrQuantShape", "make_quant_shape", "cbr_fp8_quantize", "CbrGemmShape",
+           "make_gemm_shape", "cbr_gemm_fp8_workspace_bytes", "cbr_gemm_fp8", "CBR_BF16", "CBR_F16", "CBR_F32",
+           "CBR_E4M3", "CBR_E5M2", "CBR_NORM_NONE", "CBR_NORM_RMS", "CBR_NORM_LAYER"]
 
 CBR_OP_TRAIN, CBR_OP_INFER, CBR_OP_BWD = 0, 1, 2
+CBR_BF16, CBR_F16, CBR_F32, CBR_E4M3, CBR_E5M2 = 0, 1, 2, 3, 4
+CBR_NORM_NONE, CBR_NORM_RMS, CBR_NORM_LAYER = 0, 1, 2
+_BYTES = {CBR_BF16: 2, CBR_F16: 2, CBR_F32: 4, CBR_E4M3: 1, CBR_E5M2: 1}
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libcbr.so")
 
@@ -29,6 +36,25 @@ _LIB_PATH = os.path.join(_HERE, "libcbr.so")
 class CbrShape(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int32) for name in
                 ("n", "h", "w", "c", "k", "r", "s", "stride_h", "stride_w", "pad_h", "pad_w")]
+
+
+class CbrBlockShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("rows_per_gate", ctypes.c_int64), ("channels", ctypes.c_int32),
+                ("post", ctypes.c_int32), ("pre", ctypes.c_int32), ("stream_type", ctypes.c_int32),
+                ("branch_type", ctypes.c_int32), ("alpha", ctypes.c_float), ("eps_post", ctypes.c_float),
+                ("eps_pre", ctypes.c_float)]
+
+
+class CbrQuantShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ldq", ctypes.c_int64),
+                ("src_type", ctypes.c_int32), ("q_type", ctypes.c_int32), ("transpose", ctypes.c_int32),
+                ("block", ctypes.c_int32)]
+
+
+class CbrGemmShape(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("lda", ctypes.c_int64),
+                ("ldb", ctypes.c_int64), ("a_type", ctypes.c_int32), ("b_type", ctypes.c_int32),
+                ("d_type", ctypes.c_int32), ("b_block", ctypes.c_int32), ("relu", ctypes.c_int32)]
 
 
 class CbrError(RuntimeError):
@@ -89,6 +115,16 @@ def _load():
         fn.restype = ctypes.c_int
         fe.argtypes = fn.argtypes + [P]
         fe.restype = ctypes.c_int
+    B, U, G = (ctypes.POINTER(t) for t in (CbrBlockShape, CbrQuantShape, CbrGemmShape))
+    for name, args, res in (
+            ("cbr_block_norm_workspace_bytes", [B], ctypes.c_size_t),
+            ("cbr_block_norm_forward", [B] + [P] * 13, ctypes.c_int),
+            ("cbr_block_norm_backward", [B] + [P] * 20 + [ctypes.c_size_t, P], ctypes.c_int),
+            ("cbr_fp8_quantize", [U] + [P] * 4, ctypes.c_int),
+            ("cbr_gemm_fp8_workspace_bytes", [G], ctypes.c_size_t),
+            ("cbr_gemm_fp8", [G] + [P] * 7 + [ctypes.c_size_t, P], ctypes.c_int)):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = res
     _lib = lib
     return lib
 
@@ -269,3 +305,139 @@ def cbr_conv2d_bias_relu(shape, x, w, bias, y, stream=None, events=None):
 
 def cbr_conv2d_bias(shape, x, w, bias, y, stream=None, events=None):
     _conv_bias("cbr_conv2d_bias", shape, x, w, bias, y, stream, events)
+
+
+# Element types that a tensor of each cbr_dtype may have: its own, or an integer of its size.
+_DTYPES = {CBR_BF16: ("torch.bfloat16", "torch.int16", "torch.uint16"), CBR_F16: ("torch.float16", "torch.int16", "torch.uint16"),
+           CBR_F32: ("torch.float32",), CBR_E4M3: ("torch.float8_e4m3fn", "torch.uint8", "torch.int8"),
+           CBR_E5M2: ("torch.float8_e5m2", "torch.uint8", "torch.int8")}
+_dtypes = None   # the same as sets of torch's own, made on the first call
+
+
+def _arg(t, kind, name, where, numel=None):
+    """Device address of tensor t of cbr_dtype kind, after _ptr's checks and two more: the
+    tensor's own type is that type, and it lives on the current device (the one whose stream
+    the call runs on)."""
+    global _dtypes
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if _dtypes is None:
+        _dtypes = {k: frozenset(getattr(torch, n[6:]) for n in v) for k, v in _DTYPES.items()}
+    p = _ptr(t, _BYTES[kind], name, where, numel)
+    if t.dtype not in _dtypes[kind]:
+        raise CbrError(_E_VALUE, where, f"{name} is {t.dtype}, expected {_DTYPES[kind][0]}")
+    if t.get_device() != torch.cuda.current_device():
+        raise CbrError(_E_VALUE, where, f"{name} is on GPU {t.get_device()}, the current one is "
+                                        f"{torch.cuda.current_device()}")
+    return p
+
+
+def _work(workspace, where):
+    """_ws for a workspace on the current device; None where there is none."""
+    if workspace is None or isinstance(workspace, tuple):
+        return _ws(workspace, where)
+    import torch
+    if workspace.is_cuda and workspace.get_device() != torch.cuda.current_device():
+        raise CbrError(_E_VALUE, where, "workspace is not on the current GPU")
+    return _ws(workspace, where)
+
+
+def _kinds(where, *kinds):
+    if any(k not in _BYTES for k in kinds):
+        raise CbrError(_E_VALUE, where)
+
+
+def make_block_shape(rows, channels, rows_per_gate=0, post=CBR_NORM_NONE, pre=CBR_NORM_NONE, stream_type=CBR_BF16,
+                     branch_type=CBR_BF16, alpha=1.0, eps_post=1e-5, eps_pre=1e-5) -> CbrBlockShape:
+    return CbrBlockShape(rows, rows_per_gate, channels, post, pre, stream_type, branch_type, alpha, eps_post, eps_pre)
+
+
+def cbr_block_norm_workspace_bytes(shape: CbrBlockShape) -> int:
+    return int(_load().cbr_block_norm_workspace_bytes(_sp(shape)))
+
+
+def cbr_block_norm_forward(shape, x, f, post_w, post_b, gate, res_scale, pre_w, pre_b, y, h, post_stats=None,
+                           pre_stats=None, stream=None):
+    """y = x + alpha * res_scale * gate * post(f) and h = pre(y), as include/cbr.h describes;
+    None is a pointer that is not given."""
+    w, s = "cbr_block_norm_forward", shape
+    S, B, F = s.stream_type, s.branch_type, CBR_F32
+    _kinds(w, S, B)
+    n, c, st = s.rows * s.channels, s.channels, 2 * s.rows
+    g = s.rows // s.rows_per_gate * c if s.rows_per_gate > 0 else None
+    _check(_load().cbr_block_norm_forward(
+        _sp(s), _arg(x, S, "x", w, n), _arg(f, B, "f", w, n), _arg(post_w, F, "post_w", w, c),
+        _arg(post_b, F, "post_b", w, c), _arg(gate, B, "gate", w, g), _arg(res_scale, F, "res_scale", w, c),
+        _arg(pre_w, F, "pre_w", w, c), _arg(pre_b, F, "pre_b", w, c), _arg(y, S, "y", w, n), _arg(h, B, "h", w, n),
+        _arg(post_stats, F, "post_stats", w, st), _arg(pre_stats, F, "pre_stats", w, st), _stream(stream)), w)
+
+
+def cbr_block_norm_backward(shape, dy, dh, y, f, post_w, post_b, gate, res_scale, pre_w, post_stats, pre_stats, dx, df,
+                            dpost_w, dpost_b, dgate, dres_scale, dpre_w, dpre_b, workspace, stream=None):
+    """Gradients of cbr_block_norm_forward; None is a pointer that is not given (a gradient
+    that is not wanted)."""
+    w, s = "cbr_block_norm_backward", shape
+    S, B, F = s.stream_type, s.branch_type, CBR_F32
+    _kinds(w, S, B)
+    n, c, st = s.rows * s.channels, s.channels, 2 * s.rows
+    g = s.rows // s.rows_per_gate * c if s.rows_per_gate > 0 else None
+    ws, nbytes = _work(workspace, w)
+    _check(_load().cbr_block_norm_backward(
+        _sp(s), _arg(dy, S, "dy", w, n), _arg(dh, B, "dh", w, n), _arg(y, S, "y", w, n), _arg(f, B, "f", w, n),
+        _arg(post_w, F, "post_w", w, c), _arg(post_b, F, "post_b", w, c), _arg(gate, B, "gate", w, g),
+        _arg(res_scale, F, "res_scale", w, c), _arg(pre_w, F, "pre_w", w, c),
+        _arg(post_stats, F, "post_stats", w, st), _arg(pre_stats, F, "pre_stats", w, st), _arg(dx, S, "dx", w, n),
+        _arg(df, B, "df", w, n), _arg(dpost_w, F, "dpost_w", w, c), _arg(dpost_b, F, "dpost_b", w, c),
+        _arg(dgate, B, "dgate", w, g), _arg(dres_scale, F, "dres_scale", w, c), _arg(dpre_w, F, "dpre_w", w, c),
+        _arg(dpre_b, F, "dpre_b", w, c), ws, nbytes, _stream(stream)), w)
+
+
+def make_quant_shape(rows, cols, src_type=CBR_BF16, q_type=CBR_E4M3, transpose=False, block=1,
+                     ldq=None) -> CbrQuantShape:
+    """ldq None: the row length rounded up to 16 bytes."""
+    if ldq is None:
+        ldq = -(-(rows if transpose else cols) // 16) * 16
+    return CbrQuantShape(rows, cols, ldq, src_type, q_type, int(bool(transpose)), block)
+
+
+def cbr_fp8_quantize(shape, src, q, scale, stream=None):
+    """src (or its transpose) in 8 bits, q [rows][ldq] bytes, with its scales (include/cbr.h)."""
+    w, s = "cbr_fp8_quantize", shape
+    _kinds(w, s.src_type, s.q_type)
+    if s.block not in (1, 128):
+        raise CbrError(_E_VALUE, w)
+    rows, cols = (s.cols, s.rows) if s.transpose else (s.rows, s.cols)
+    _check(_load().cbr_fp8_quantize(_sp(s), _arg(src, s.src_type, "src", w, s.rows * s.cols),
+                                    _arg(q, s.q_type, "q", w, (rows - 1) * s.ldq + cols),
+                                    _arg(scale, CBR_F32, "scale", w, -(-cols // 128) * -(-rows // s.block)),
+                                    _stream(stream)), w)
+
+
+def make_gemm_shape(m, n, k, a_type=CBR_E4M3, b_type=CBR_E4M3, d_type=CBR_BF16, b_block=128, relu=False, lda=None,
+                    ldb=None) -> CbrGemmShape:
+    """lda, ldb None: k rounded up to 16 bytes."""
+    ld = -(-k // 16) * 16
+    return CbrGemmShape(m, n, k, ld if lda is None else lda, ld if ldb is None else ldb, a_type, b_type, d_type,
+                        b_block, int(bool(relu)))
+
+
+def cbr_gemm_fp8_workspace_bytes(shape: CbrGemmShape) -> int:
+    return int(_load().cbr_gemm_fp8_workspace_bytes(_sp(shape)))
+
+
+def cbr_gemm_fp8(shape, a, a_scale, b, b_scale, bias, d, workspace=None, stream=None):
+    """d = act((a * a_scale) (b * b_scale)^T + bias) of 8-bit operands (include/cbr.h); workspace
+    may be None where cbr_gemm_fp8_workspace_bytes is 0."""
+    w, s = "cbr_gemm_fp8", shape
+    _kinds(w, s.a_type, s.b_type, s.d_type)
+    if s.b_block not in (1, 128):
+        raise CbrError(_E_VALUE, w)
+    kb = -(-s.k // 128)
+    ws, nbytes = _work(workspace, w)
+    _check(_load().cbr_gemm_fp8(_sp(s), _arg(a, s.a_type, "a", w, s.m * s.lda),
+                                _arg(a_scale, CBR_F32, "a_scale", w, kb * s.m),
+                                _arg(b, s.b_type, "b", w, s.n * s.ldb),
+                                _arg(b_scale, CBR_F32, "b_scale", w, kb * -(-s.n // s.b_block)),
+                                _arg(bias, CBR_F32, "bias", w, s.n), _arg(d, s.d_type, "d", w, s.m * s.n),
+                                ws, nbytes, _stream(stream)), w)

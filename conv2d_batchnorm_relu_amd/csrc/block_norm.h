@@ -1,0 +1,140 @@
+// block_norm.h -- device pieces shared by the block norm's forward and backward kernels:
+// how a row's channels lie in the threads, and sums over a row.
+#pragma once
+
+#include "block_launch.h"
+#include "block_types.h"
+
+namespace cbr {
+namespace bnorm {
+
+// A row is held by L threads, E values each (8 or 16): L a power of two up to 64 (then
+// several rows share a wave), or a multiple of 64 (several waves share a row).  Thread l's
+// values 8i..8i+7 are channels 8 (i L + l) .. + 7, one 16- or 32-byte access.  TAIL (C % 8
+// != 0): rows start at any value's address and the last chunk of a row is a part of one.
+template <int E>
+__device__ __forceinline__ int col_of(int j, int l, int L)
+{
+    return 8 * ((j >> 3) * L + l) + (j & 7);
+}
+
+// Whether value j exists (!TAIL: the same answer for the eight values of a chunk).
+template <int E, bool TAIL>
+__device__ __forceinline__ bool has(int j, int l, int L, int C)
+{
+    return col_of<E>(TAIL ? j : (j & ~7), l, L) < C;
+}
+
+// A thread's values of one row of a tensor of type T, as they sit in memory.
+template <typename T, int E, bool TAIL>
+struct Row {
+    Raw8<T> c[E / 8];
+
+    // row: byte address of the row's channel 0; on false nothing is read and the values are 0
+    __device__ __forceinline__ void load(const char *row, int l, int L, int C, bool on)
+    {
+#pragma unroll
+        for (int i = 0; i < E / 8; ++i) {
+            const int col = 8 * (i * L + l);
+            const char *p = row + (size_t)col * T::SIZE;
+            if (on && col + (TAIL ? 8 : 1) <= C) load_raw8<T, TAIL>(p, c[i]);
+            else if (TAIL && on && col < C) load_part8<T>(p, C - col, c[i]);
+            else c[i] = Raw8<T>{};
+        }
+    }
+
+    __device__ __forceinline__ void get(float (&o)[E]) const
+    {
+#pragma unroll
+        for (int i = 0; i < E / 8; ++i) unpack8<T>(c[i], o + 8 * i);
+    }
+
+    static __device__ __forceinline__ void store(char *row, int l, int L, int C, const float (&v)[E])
+    {
+#pragma unroll
+        for (int i = 0; i < E / 8; ++i) {
+            const int col = 8 * (i * L + l);
+            char *p = row + (size_t)col * T::SIZE;
+            if (col + (TAIL ? 8 : 1) <= C) {
+                Raw8<T> r;
+                pack8<T>(v + 8 * i, r);
+                store_raw8<T, TAIL>(p, r);
+            } else if (TAIL && col < C) {
+                store_part8<T>(p, C - col, v + 8 * i);
+            }
+        }
+    }
+};
+
+// A float vector of the channels, `none` where it is not given.
+template <int E, bool TAIL>
+__device__ __forceinline__ void load_vec(const float *p, float none, int l, int L, int C, float (&o)[E])
+{
+    if (p) {
+        Row<F32, E, TAIL> r;
+        r.load((const char *)p, l, L, C, true);
+        r.get(o);
+    } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j) o[j] = none;
+    }
+}
+
+constexpr int MAX_WAVES = 16;
+
+// Sums over the L threads of each row, for all rows of the workgroup at once: lane shuffles
+// within a wave (both operands of an addition are the same at both lanes, so every lane
+// holds the same sum), then, for rows of several waves, the waves' sums through LDS in wave
+// order.  Two halves of `red` take turns: a wave that is past the barrier of one sum may
+// write the next, never the one that others still read.
+template <int NV>
+struct RowSum {
+    float (*red)[MAX_WAVES][NV];   // [2][MAX_WAVES][NV]
+    int L, turn;
+
+    __device__ __forceinline__ void operator()(float (&v)[NV])
+    {
+        const int w = L < 64 ? L : 64;
+        for (int off = 1; off < w; off <<= 1)
+#pragma unroll
+            for (int e = 0; e < NV; ++e) v[e] += __shfl_xor(v[e], off);
+        if (L > 64) {
+            const int wave = threadIdx.x >> 6, per = L >> 6, first = wave / per * per;
+            if ((threadIdx.x & 63) == 0)
+#pragma unroll
+                for (int e = 0; e < NV; ++e) red[turn][wave][e] = v[e];
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < NV; ++e) v[e] = red[turn][first][e];
+            for (int i = 1; i < per; ++i)
+#pragma unroll
+                for (int e = 0; e < NV; ++e) v[e] += red[turn][first + i][e];
+            turn ^= 1;
+        }
+    }
+};
+
+// How rows of C channels lie in a workgroup of about `most` threads: eight values a thread
+// (one 16-byte access of a 2-byte type) where a row then fits the workgroup, else sixteen.
+struct Layout {
+    int E, L, rpb, threads;   // values a thread, threads a row, rows a workgroup
+    bool tail;
+};
+
+inline Layout layout_of(int C, int most, int limit)
+{
+    Layout o;
+    o.tail = C % 8 != 0;
+    o.E = (C + 7) / 8 <= limit ? 8 : 16;
+    const int n = (C + o.E - 1) / o.E;
+    o.L = 1;
+    if (n > 64) o.L = (n + 63) / 64 * 64;
+    else
+        while (o.L < n) o.L *= 2;
+    o.rpb = o.L >= most ? 1 : most / o.L;
+    o.threads = o.L * o.rpb;
+    return o;
+}
+
+}  // namespace bnorm
+}  // namespace cbr

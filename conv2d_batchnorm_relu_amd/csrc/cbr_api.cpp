@@ -208,7 +208,7 @@ const char *cbr_status_str(int status)
     case CBR_E_ALIGN: return "CBR_E_ALIGN: a tensor pointer is not 16-byte aligned";
     case CBR_E_WORKSPACE: return "CBR_E_WORKSPACE: workspace missing or too small";
     case CBR_E_HIP: return "CBR_E_HIP: a kernel launch failed";
-    case CBR_E_VALUE: return "CBR_E_VALUE: eps or momentum out of range";
+    case CBR_E_VALUE: return "CBR_E_VALUE: a value is out of range (eps, momentum, a type or kind), or an argument does not fit the others";
     default: return "CBR: unknown status";
     }
 }

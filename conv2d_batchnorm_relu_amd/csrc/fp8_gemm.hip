@@ -1,0 +1,577 @@
+// fp8_gemm.hip -- matrix product of 8-bit operands with a scale for each block of 128:
+//   d[m][n] = act( sum_t sa[t][m] sb[t][n / b_block] * sum_{k in block t} a[m][k] b[n][k] + bias[n] )
+//
+// A block of 128 is summed by matrix instructions that start from zero; its results are then
+// scaled and added to the fp32 sums by the vector unit.  The filter side (b) is the
+// instruction's A operand and the activations (a) its B operand, so a lane's four results are
+// consecutive n of one m: one scale for all of them when b has 128 x 128 blocks, and one 8- or
+// 16-byte store.  Both operands hold k in the same order within a lane, which is all the
+// product asks of that order.
+//
+// Two ways to sum a block:
+//   * v_mfma_f32_16x16x128_f8f6f4, one instruction for the block, 16-bit outputs.  It aligns
+//     the eight products of each 8 consecutive k to the largest of them and keeps 13 bits
+//     below its leading one (measured; between eights it adds in fp32).  On normal values that
+//     is 1.3e-5 of the result's norm, 130 times below the rounding to bf16 and 16 below f16.
+//   * operands widened to bf16 (exactly) and four v_mfma_f32_16x16x32_bf16, whose sums are
+//     fp32 throughout (same probe), at half the rate: fp32 outputs, and few rows, where
+//     reading b bounds the call.
+#include <type_traits>
+
+#include "block_launch.h"
+#include "block_types.h"
+
+namespace cbr {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+constexpr int BK = 128;              // bytes of k in a block, and of an LDS row
+constexpr uint32_t OOB = 0x80000000u;
+
+struct GemmArgs {
+    const uint8_t *a, *b;
+    const float *sa, *sb, *bias;
+    void *d;
+    float *part;        // [splits][M][N], where the k blocks are shared out
+    int64_t M;
+    int N, K, lda, ldb;
+    int kbs;            // blocks of k
+    int kb_per;         // blocks of k a split takes
+    int sb_ld;          // scales of b in a block of k
+    int d_type, relu;
+    int tiles_m, tiles_n;
+};
+
+struct __attribute__((packed, aligned(2))) Loose8 {
+    uint2 v;
+};
+struct __attribute__((packed, aligned(4))) LooseF4 {
+    f32x4 v;
+};
+
+// One product of 16 x 16 over 128 values: FB, FA the formats of b and a (0 e4m3, 1 e5m2).
+// Unit scales: the instruction's own (powers of two for 32 values) are not used.
+template <int FB, int FA>
+__device__ __forceinline__ f32x4 product(const i32x8 &b, const i32x8 &a)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, f32x4{0.f, 0.f, 0.f, 0.f}, FB, FA, 0, 0, 0, 0);
+}
+
+// Eight 8-bit values (F: 0 e4m3, 1 e5m2) as bf16, exactly.
+template <int F>
+__device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi)
+{
+    bf16x2 p[4];
+    if constexpr (F == 0) {
+        p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
+        p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
+        p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
+        p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+    } else {
+        p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.f, false);
+        p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.f, true);
+        p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.f, false);
+        p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.f, true);
+    }
+    bf16x8 v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = p[e / 2][e % 2];
+    return v;
+}
+
+// A lane's 32 values of a row of a block, widened: value set t holds bytes 8t..8t+7.
+template <int F>
+struct Wide {
+    bf16x8 t[4];
+    __device__ __forceinline__ void set(u32x4 lo, u32x4 hi)
+    {
+        t[0] = widen8<F>(lo[0], lo[1]);
+        t[1] = widen8<F>(lo[2], lo[3]);
+        t[2] = widen8<F>(hi[0], hi[1]);
+        t[3] = widen8<F>(hi[2], hi[3]);
+    }
+};
+
+__device__ __forceinline__ f32x4 product(const bf16x8 &b, const bf16x8 &a, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi)
+{
+    return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// f(integral_constant 0), ... f(integral_constant N - 1)
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unrolled(F &&f)
+{
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        unrolled<N, I + 1>(f);
+    }
+}
+
+// LDS reads in inline assembly, as in the convolutions: with global-to-LDS loads in flight
+// the compiler would wait for all of them before any LDS read of its own.
+template <int OFF>
+__device__ __forceinline__ u32x4 lds_read16(uint32_t addr)
+{
+    u32x4 v;
+    asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFF) : "memory");
+    return v;
+}
+template <int N>
+__device__ __forceinline__ void lgkm_wait()
+{
+    asm volatile("s_waitcnt lgkmcnt(%0)" : : "i"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void vm_wait()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" : : "i"(N) : "memory");
+}
+__device__ __forceinline__ void after_wait(u32x4 &x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void buffer_load_lds16(__amdgpu_buffer_rsrc_t r, lds_u8 *dst, int voff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, voff, 0, 0, 0);
+}
+
+// Four results of consecutive n at (m, n): bias, activation, rounding, store.
+__device__ __forceinline__ void finish4(const GemmArgs &p, int64_t m, int n, f32x4 v)
+{
+    const int left = p.N - n;   // > 0
+    if (p.bias) {
+        if (left >= 4) v += *(const f32x4 *)(p.bias + n);   // n is a multiple of 4
+        else
+            for (int e = 0; e < 3; ++e)
+                if (e < left) v[e] += p.bias[n + e];
+    }
+    if (p.relu)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = v[e] < 0.f ? 0.f : v[e];   // a NaN stays one
+    const int64_t at = m * p.N + n;
+    if (p.d_type == CBR_F32) {
+        float *o = (float *)p.d + at;
+        if (left >= 4) ((LooseF4 *)o)->v = v;
+        else
+            for (int e = 0; e < 3; ++e)
+                if (e < left) o[e] = v[e];
+        return;
+    }
+    const bool half = p.d_type == CBR_F16;
+    const uint2 w = half ? make_uint2(F16::pack(v[0], v[1]), F16::pack(v[2], v[3]))
+                         : make_uint2(Bf16::pack(v[0], v[1]), Bf16::pack(v[2], v[3]));
+    uint16_t *o = (uint16_t *)p.d + at;
+    if (left >= 4) ((Loose8 *)o)->v = w;
+    else
+        for (int e = 0; e < 3; ++e)
+            if (e < left) o[e] = (uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
+}
+
+__device__ __forceinline__ void emit4(const GemmArgs &p, int64_t m, int n, f32x4 v)
+{
+    if (p.part) {
+        float *o = p.part + ((int64_t)blockIdx.y * p.M + m) * p.N + n;
+        if (n + 4 <= p.N) ((LooseF4 *)o)->v = v;
+        else
+            for (int e = 0; e < 3; ++e)
+                if (n + e < p.N) o[e] = v[e];
+    } else {
+        finish4(p, m, n, v);
+    }
+}
+
+// The scales of b for four consecutive n of block kb (BB 1).
+__device__ __forceinline__ f32x4 scale4(const GemmArgs &p, int kb, int n)
+{
+    const float *s = p.sb + (int64_t)kb * p.sb_ld;
+    if (n + 4 <= p.N) return ((const LooseF4 *)(s + n))->v;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+        if (n + e < p.N) v[e] = s[n + e];
+    return v;
+}
+
+// Tile kernel: 16 MS WM x 16 NS WN results a workgroup, WM x WN waves of 16 MS x 16 NS.
+// Both operands' rows of a k block (128 bytes) come straight into LDS, two blocks deep:
+// block t + 1 loads while block t is multiplied.  16-byte chunk c of row r lies at
+// c ^ ((r / 2) % 8), so the sixteen rows of a fragment read fall on all 64 banks.
+// WIDE: through bf16.
+template <int MS, int NS, int WM, int WN, int FA, int FB, int BB, bool WIDE>
+__global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
+{
+    constexpr int NW = WM * WN, BM = 16 * MS * WM, BN = 16 * NS * WN;
+    constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;   // load instructions a wave, 8 rows each
+    constexpr int STAGE = (BM + BN) * BK;
+    static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN && NW >= 2, "tile shape");
+    static_assert(BB == 1 || 128 % (16 * NS) == 0, "a wave's columns lie in one block of b");
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const uint32_t lbase = (uint32_t)(uintptr_t)(lds_u8 *)lds;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane & 15, g = lane >> 4;
+    const int wm = wave / WN, wn = wave % WN;
+
+    const int tm = blockIdx.x % p.tiles_m, tn = blockIdx.x / p.tiles_m;
+    const int64_t m0 = (int64_t)tm * BM;
+    const int n0 = tn * BN;
+    const int kb0 = blockIdx.y * p.kb_per, kb1 = min(p.kbs, kb0 + p.kb_per);
+
+    // rows past the end of an operand lie past the end of its buffer and read as zeros
+    const int rows_a = (int)min((int64_t)BM, p.M - m0), rows_b = min(BN, p.N - n0);
+    const __amdgpu_buffer_rsrc_t ra =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(p.a + m0 * p.lda), 0, rows_a * p.lda, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rb =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(p.b + (int64_t)n0 * p.ldb), 0, rows_b * p.ldb, 0x00020000);
+    const int lrow = 8 * wave + (lane >> 3);
+    const int lchunk = 16 * ((lane & 7) ^ ((lrow >> 1) & 7));
+    auto load = [&](int kb) __attribute__((always_inline)) {
+        const int kat = kb * BK + lchunk;
+        const bool in = kat < p.K;   // a chunk past K is not read: zeros
+        lds_u8 *dst = (lds_u8 *)lds + (kb & 1) * STAGE + wave * 1024;
+#pragma unroll
+        for (int t = 0; t < LA; ++t)
+            buffer_load_lds16(ra, dst + t * NW * 1024, in ? (lrow + t * 8 * NW) * p.lda + kat : (int)OOB);
+#pragma unroll
+        for (int t = 0; t < LB; ++t)
+            buffer_load_lds16(rb, dst + BM * BK + t * NW * 1024, in ? (lrow + t * 8 * NW) * p.ldb + kat : (int)OOB);
+    };
+
+    // this lane's rows of a and columns of b
+    const int64_t mw = m0 + wm * 16 * MS + r16;
+    const int nw = n0 + wn * 16 * NS;
+    const int nl = nw + 4 * g;
+    float sa[MS];
+    f32x4 sb[BB == 1 ? NS : 1];
+    auto scales = [&](int kb) __attribute__((always_inline)) {
+        const float *s = p.sa + (int64_t)kb * p.M;
+#pragma unroll
+        for (int j = 0; j < MS; ++j) sa[j] = s[min(mw + 16 * j, p.M - 1)];
+        if constexpr (BB == 1) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) sb[i] = scale4(p, kb, nl + 16 * i);
+        } else {
+            sb[0][0] = p.sb[(int64_t)kb * p.sb_ld + min(nw, p.N - 1) / 128];
+        }
+    };
+
+    f32x4 acc[NS][MS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int j = 0; j < MS; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const uint32_t fa0 = lbase + (wm * 16 * MS + r16) * BK + 16 * (g ^ ((r16 >> 1) & 7));
+    const uint32_t fb0 = lbase + BM * BK + (wn * 16 * NS + r16) * BK + 16 * (g ^ ((r16 >> 1) & 7));
+
+    load(kb0);
+    scales(kb0);
+    for (int kb = kb0; kb < kb1; ++kb) {
+        vm_wait<0>();
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (kb + 1 == p.kbs && (p.K & 15)) {
+            // the chunk that K ends in: clear what lies past it (block b of 128 ends at K)
+            const int kl = p.K - kb * BK, c = kl >> 4, cut = kl & 15;
+            for (int r = threadIdx.x; r < BM + BN; r += 64 * NW) {
+                u32x4 *q = (u32x4 *)(lds + (kb & 1) * STAGE + r * BK + 16 * (c ^ ((r >> 1) & 7)));
+                u32x4 v = *q;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int keep = cut - 4 * e;   // bytes of this word
+                    v[e] = keep >= 4 ? v[e] : keep <= 0 ? 0u : v[e] & ((1u << (8 * keep)) - 1u);
+                }
+                *q = v;
+            }
+            __syncthreads();
+        }
+        float s[MS];
+        f32x4 t4[BB == 1 ? NS : 1];
+#pragma unroll
+        for (int j = 0; j < MS; ++j) s[j] = BB == 1 ? sa[j] : sa[j] * sb[0][0];
+        if constexpr (BB == 1)
+#pragma unroll
+            for (int i = 0; i < NS; ++i) t4[i] = sb[i];
+        if (kb + 1 < kb1) {
+            scales(kb + 1);
+            load(kb + 1);
+        }
+        const uint32_t fa = fa0 + (kb & 1) * STAGE, fb = fb0 + (kb & 1) * STAGE;
+        u32x4 bf[NS][2], af[3][2];
+        unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
+            constexpr int i = decltype(ic)::value;
+            bf[i][0] = lds_read16<i * 16 * BK>(fb);
+            bf[i][1] = lds_read16<i * 16 * BK>(fb ^ 64);
+        });
+        af[0][0] = lds_read16<0>(fa);
+        af[0][1] = lds_read16<0>(fa ^ 64);
+        if constexpr (MS > 1) {
+            af[1][0] = lds_read16<16 * BK>(fa);
+            af[1][1] = lds_read16<16 * BK>(fa ^ 64);
+        }
+        f32x4 q[NS];
+        Wide<FB> wb[WIDE ? NS : 1];
+        auto add = [&](int i, int j) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[i][j][e] = fmaf(BB == 1 ? q[i][e] * t4[BB == 1 ? i : 0][e] : q[i][e], s[j], acc[i][j][e]);
+        };
+        unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
+            constexpr int J = decltype(jc)::value;
+            lgkm_wait<(J + 1 < MS ? 2 : 0)>();   // all but the next fragment of a
+            if constexpr (J == 0)
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    after_wait(bf[i][0]);
+                    after_wait(bf[i][1]);
+                }
+            after_wait(af[J % 3][0]);
+            after_wait(af[J % 3][1]);
+            if constexpr (J + 2 < MS) {
+                af[(J + 2) % 3][0] = lds_read16<(J + 2) * 16 * BK>(fa);
+                af[(J + 2) % 3][1] = lds_read16<(J + 2) * 16 * BK>(fa ^ 64);
+            }
+            if constexpr (WIDE) {
+                if constexpr (J == 0)
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) wb[i].set(bf[i][0], bf[i][1]);
+                Wide<FA> wa;
+                wa.set(af[J % 3][0], af[J % 3][1]);
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) {
+                        if (J > 0 && t == 0) add(i, J - 1);
+                        q[i] = product(wb[i].t[t], wa.t[t], t == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : q[i]);
+                    }
+            } else {
+                const i32x8 av = join(af[J % 3][0], af[J % 3][1]);
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    if constexpr (J > 0) add(i, J - 1);
+                    q[i] = product<FB, FA>(join(bf[i][0], bf[i][1]), av);
+                }
+            }
+        });
+#pragma unroll
+        for (int i = 0; i < NS; ++i) add(i, MS - 1);
+        // every wave has read this block before block kb + 2 overwrites it: the barrier of
+        // the next turn, which this wave reaches with its reads done (the products used them)
+    }
+#pragma unroll
+    for (int j = 0; j < MS; ++j) {
+        const int64_t m = mw + 16 * j;
+        if (m >= p.M) continue;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            if (nl + 16 * i < p.N) emit4(p, m, nl + 16 * i, acc[i][j]);
+    }
+}
+
+// Few rows of a (m <= 16 MS): bound by reading b once.  A workgroup takes 16 columns, its
+// eight waves share the blocks of k, and both operands come from memory straight into the
+// product's registers (a row's 128 bytes of a block are read by four lanes, 32 each); the
+// waves' sums are added through LDS in wave order.
+constexpr int SKW = 8;
+
+template <int MS, int FA, int FB, int BB>
+__global__ __launch_bounds__(64 * SKW) void gemm_few_kernel(GemmArgs p)
+{
+    __shared__ f32x4 red[SKW][MS][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane & 15, g = lane >> 4;
+    const int n0 = blockIdx.x * 16, nl = n0 + 4 * g;
+    const int kb0 = blockIdx.y * p.kb_per, kb1 = min(p.kbs, kb0 + p.kb_per);
+    // rows past the end read the last one; their results are not stored
+    const uint8_t *brow = p.b + (int64_t)min(n0 + r16, p.N - 1) * p.ldb + 32 * g;
+    const uint8_t *arow[MS];
+    int mrow[MS];
+#pragma unroll
+    for (int j = 0; j < MS; ++j) {
+        mrow[j] = min(16 * j + r16, (int)p.M - 1);
+        arow[j] = p.a + (int64_t)mrow[j] * p.lda + 32 * g;
+    }
+    f32x4 acc[MS];
+#pragma unroll
+    for (int j = 0; j < MS; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto block = [&](int kb, auto &&get) __attribute__((always_inline)) {
+        Wide<FB> wb;
+        u32x4 lo, hi;
+        get(brow + kb * BK, lo, hi);
+        wb.set(lo, hi);
+        f32x4 sb;
+        if constexpr (BB == 1) sb = scale4(p, kb, nl);
+        else sb[0] = p.sb[(int64_t)kb * p.sb_ld + n0 / 128];
+#pragma unroll
+        for (int j = 0; j < MS; ++j) {
+            Wide<FA> wa;
+            get(arow[j] + kb * BK, lo, hi);
+            wa.set(lo, hi);
+            f32x4 q = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t < 4; ++t) q = product(wb.t[t], wa.t[t], q);
+            const float s = p.sa[(int64_t)kb * p.M + mrow[j]];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(q[e] * sb[BB == 1 ? e : 0], s, acc[j][e]);
+        }
+    };
+    auto whole = [](const uint8_t *q, u32x4 &lo, u32x4 &hi) __attribute__((always_inline)) {
+        lo = *(const u32x4 *)q;
+        hi = *(const u32x4 *)(q + 16);
+    };
+    const int full = min(kb1, p.K / BK);   // blocks that K does not end in
+    for (int kb = kb0 + wave; kb < full; kb += SKW) block(kb, whole);
+    const int last = p.K / BK;
+    if (last >= kb0 && last < kb1 && (last - kb0) % SKW == wave && p.K % BK) {
+        const int left = p.K - last * BK - 32 * g;   // bytes of this lane's 32
+        block(last, [&](const uint8_t *q, u32x4 &lo, u32x4 &hi) __attribute__((always_inline)) {
+            lo = left > 0 ? *(const u32x4 *)q : u32x4{0u, 0u, 0u, 0u};
+            hi = left > 16 ? *(const u32x4 *)(q + 16) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int keep = left - 4 * e;
+                const uint32_t w = e < 4 ? lo[e % 4] : hi[e % 4];
+                const uint32_t c = keep >= 4 ? w : keep <= 0 ? 0u : w & ((1u << (8 * keep)) - 1u);
+                if (e < 4) lo[e % 4] = c;
+                else hi[e % 4] = c;
+            }
+        });
+    }
+#pragma unroll
+    for (int j = 0; j < MS; ++j) red[wave][j][lane] = acc[j];
+    __syncthreads();
+    for (int j = wave; j < MS; j += SKW) {
+        f32x4 v = red[0][j][lane];
+#pragma unroll
+        for (int w = 1; w < SKW; ++w) v += red[w][j][lane];
+        const int m = 16 * j + r16;
+        if (m < p.M && nl < p.N) emit4(p, m, nl, v);
+    }
+}
+
+// The splits' parts, added in order, and the epilogue.
+__global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs p, int splits)
+{
+    const int q4 = (p.N + 3) / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t m = i / q4;
+    const int n = (int)(i % q4) * 4;
+    if (m >= p.M) return;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    const float *o = p.part + m * p.N + n;
+    const int64_t step = p.M * p.N;
+    if (n + 4 <= p.N) {
+        for (int s = 0; s < splits; ++s) v += ((const LooseF4 *)(o + s * step))->v;
+    } else {
+        for (int s = 0; s < splits; ++s)
+            for (int e = 0; e < 3; ++e)
+                if (n + e < p.N) v[e] += o[s * step + e];
+    }
+    finish4(p, m, n, v);
+}
+
+// ------------------------------------------------------------------------------ plan
+enum Form { FEW, TILE128, TILE256 };
+
+struct GemmPlan {
+    Form form;
+    int ms;          // FEW: 16-row tiles
+    int bm, bn;
+    int splits, kb_per;
+};
+
+GemmPlan plan_of(const cbr_gemm_shape &s)
+{
+    const int64_t kbs = (s.k + BK - 1) / BK;
+    auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    GemmPlan p{};
+    int64_t tiles, min_kb;
+    if (s.m <= 64) {
+        p.form = FEW;
+        p.ms = s.m <= 16 ? 1 : s.m <= 32 ? 2 : 4;
+        p.bm = 16 * p.ms;
+        p.bn = 16;
+        min_kb = 2 * SKW;
+    } else {
+        const bool big = s.d_type != CBR_F32 && up(s.m, 256) * up(s.n, 256) >= 256;
+        p.form = big ? TILE256 : TILE128;
+        p.bm = p.bn = big ? 256 : 128;
+        min_kb = 8;
+    }
+    tiles = up(s.m, p.bm) * up(s.n, p.bn);
+    // Share k out until there is a workgroup for every CU, while each keeps min_kb blocks.
+    int64_t splits = 1;
+    if (tiles < 256) splits = std::max<int64_t>(1, std::min(256 / tiles, kbs / min_kb));
+    p.kb_per = (int)up(kbs, splits);
+    p.splits = (int)up(kbs, p.kb_per);
+    return p;
+}
+
+template <int FA, int FB, int BB>
+hipError_t launch_formats(const GemmPlan &pl, const GemmArgs &a, hipStream_t st)
+{
+    if (pl.form == FEW) {
+        auto k = pl.ms == 1 ? gemm_few_kernel<1, FA, FB, BB>
+                 : pl.ms == 2 ? gemm_few_kernel<2, FA, FB, BB> : gemm_few_kernel<4, FA, FB, BB>;
+        return launch(k, dim3(a.tiles_n, pl.splits), dim3(64 * SKW), 0, st, nullptr, nullptr, a);
+    }
+    const bool big = pl.form == TILE256;
+    auto k = a.d_type == CBR_F32 ? gemm_tile_kernel<4, 4, 2, 2, FA, FB, BB, true>
+             : big ? gemm_tile_kernel<8, 4, 2, 4, FA, FB, BB, false> : gemm_tile_kernel<4, 4, 2, 2, FA, FB, BB, false>;
+    const int lds = 2 * (pl.bm + pl.bn) * BK;
+    const hipError_t e = raise_lds_limit((const void *)k, lds);
+    if (e != hipSuccess) return e;
+    return launch(k, dim3((uint32_t)(a.tiles_m * a.tiles_n), pl.splits), dim3(big ? 512 : 256), lds, st, nullptr, nullptr,
+                  a);
+}
+
+}  // namespace
+
+size_t gemm_fp8_part_bytes(const cbr_gemm_shape &s)
+{
+    const GemmPlan p = plan_of(s);
+    return p.splits > 1 ? (size_t)p.splits * s.m * s.n * sizeof(float) : 0;
+}
+
+hipError_t launch_gemm_fp8(const cbr_gemm_shape &s, const void *a, const float *a_scale, const void *b,
+                           const float *b_scale, const float *bias, void *d, float *part, hipStream_t st)
+{
+    const GemmPlan pl = plan_of(s);
+    GemmArgs p{};
+    p.a = (const uint8_t *)a;
+    p.b = (const uint8_t *)b;
+    p.sa = a_scale;
+    p.sb = b_scale;
+    p.bias = bias;
+    p.d = d;
+    p.part = pl.splits > 1 ? part : nullptr;
+    p.M = s.m;
+    p.N = (int)s.n;
+    p.K = (int)s.k;
+    p.lda = (int)s.lda;
+    p.ldb = (int)s.ldb;
+    p.kbs = (int)((s.k + BK - 1) / BK);
+    p.kb_per = pl.kb_per;
+    p.sb_ld = (int)((s.n + s.b_block - 1) / s.b_block);
+    p.d_type = s.d_type;
+    p.relu = s.relu;
+    p.tiles_m = (int)((s.m + pl.bm - 1) / pl.bm);
+    p.tiles_n = (int)((s.n + pl.bn - 1) / pl.bn);
+    const bool a5 = s.a_type == CBR_E5M2, b5 = s.b_type == CBR_E5M2;
+    hipError_t e;
+    if (s.b_block == 128)
+        e = a5 ? (b5 ? launch_formats<1, 1, 128>(pl, p, st) : launch_formats<1, 0, 128>(pl, p, st))
+               : (b5 ? launch_formats<0, 1, 128>(pl, p, st) : launch_formats<0, 0, 128>(pl, p, st));
+    else
+        e = a5 ? (b5 ? launch_formats<1, 1, 1>(pl, p, st) : launch_formats<1, 0, 1>(pl, p, st))
+               : (b5 ? launch_formats<0, 1, 1>(pl, p, st) : launch_formats<0, 0, 1>(pl, p, st));
+    if (e != hipSuccess || pl.splits == 1) return e;
+    const int64_t quads = s.m * ((s.n + 3) / 4);
+    return launch(gemm_join_kernel, dim3((uint32_t)((quads + 255) / 256)), dim3(256), 0, st, nullptr, nullptr, p, pl.splits);
+}
+
+}  // namespace cbr

@@ -65,7 +65,8 @@ enum cbr_status {
     CBR_E_ALIGN = 4,        /* a tensor pointer is not 16-byte aligned               */
     CBR_E_WORKSPACE = 5,    /* workspace NULL or smaller than cbr_workspace_bytes    */
     CBR_E_HIP = 6,          /* a kernel launch failed                                */
-    CBR_E_VALUE = 7         /* eps < 0, momentum outside [0,1], or not finite        */
+    CBR_E_VALUE = 7         /* eps < 0, momentum outside [0,1], or not finite; an unknown
+                               type or kind, or an argument that does not fit the others */
 };
 
 enum cbr_op { CBR_OP_TRAIN = 0, CBR_OP_INFER = 1, CBR_OP_BWD = 2 };
@@ -204,6 +205,151 @@ int cbr_conv2d_bias_relu(const cbr_shape *shape, const uint16_t *x, const uint16
  */
 int cbr_conv2d_bias(const cbr_shape *shape, const uint16_t *x, const uint16_t *w, const float *bias,
                     uint16_t *y, void *stream);
+
+/*
+ * Norms before and after a block, with its gate and residual scale
+ * ----------------------------------------------------------------
+ * A block (convolutions, a product, ...) maps activations to a branch f; the residual
+ * stream x takes it in.  Rows are pixels (or tokens): rows x channels, dense, NHWC order,
+ * so N*H*W rows.  Row m belongs to gate row i = m / rows_per_gate (H*W: a gate an image;
+ * 1: a gate of its own for every row).  One pass over x and f computes
+ *   n    = post(f)                       norm after the block, per row, or f itself
+ *   y    = x + alpha * r_c * g_ic * n    gated and scaled residual add      stream (out)
+ *   h    = pre(y)                        norm before the next block, per row  branch (out)
+ * with the norms
+ *   CBR_NORM_LAYER: (v - mean) / sqrt(var + eps) * w + b   (var biased, over the channels)
+ *   CBR_NORM_RMS:    v / sqrt(mean of v^2 + eps) * w + b
+ *   CBR_NORM_NONE:  n = f;  as `pre`: there is no h.
+ * Everything is computed in fp32 and rounded once per output; h uses y before its rounding.
+ * Types: x, y, dx, dy have stream_type; f, h, gate and their gradients branch_type; both
+ * are CBR_BF16, CBR_F16 or CBR_F32, and they are equal or stream_type is CBR_F32.
+ * w, b, r, their gradients and the statistics are float.
+ *
+ * Limits: rows < 2^31, channels <= 8192 (any, odd ones too), rows a multiple of
+ * rows_per_gate.  channels % 8 == 0 takes 16-byte accesses.  Rows and channels must be
+ * positive (CBR_E_SHAPE).
+ */
+enum cbr_dtype { CBR_BF16 = 0, CBR_F16 = 1, CBR_F32 = 2, CBR_E4M3 = 3, CBR_E5M2 = 4 };
+enum cbr_norm { CBR_NORM_NONE = 0, CBR_NORM_RMS = 1, CBR_NORM_LAYER = 2 };
+
+typedef struct cbr_block_shape {
+    int64_t rows;
+    int64_t rows_per_gate;          /* read only where a gate is given                */
+    int32_t channels;
+    int32_t post, pre;              /* enum cbr_norm                                  */
+    int32_t stream_type, branch_type;   /* enum cbr_dtype                             */
+    float alpha;                    /* constant factor of the branch (1: none)        */
+    float eps_post, eps_pre;
+} cbr_block_shape;
+
+/* Workspace bytes of cbr_block_norm_backward; 0 for an invalid shape.  The forward needs
+ * none. */
+size_t cbr_block_norm_workspace_bytes(const cbr_block_shape *shape);
+
+/*
+ * Forward.  f may be NULL: then post is CBR_NORM_NONE, gate, res_scale and y are NULL and
+ * h = pre(x) (a first block's norm).  pre CBR_NORM_NONE: pre_w, pre_b, h and pre_stats are
+ * NULL (a last block's residual add).  post_w, post_b, pre_w, pre_b [channels], gate
+ * [rows / rows_per_gate][channels] and res_scale [channels] may each be NULL (1, or 0 for
+ * the biases); weights without their norm are refused (CBR_E_VALUE), as is a call with
+ * neither f nor pre.  post_stats, pre_stats: float [rows][2], (mean, 1/std) of each row
+ * (mean 0 for RMS), for the backward; NULL skips them (inference).
+ * y may alias x and h may alias f (same type and place); no other output may alias an input.
+ */
+int cbr_block_norm_forward(const cbr_block_shape *shape, const void *x, const void *f,
+                           const float *post_w, const float *post_b, const void *gate,
+                           const float *res_scale, const float *pre_w, const float *pre_b,
+                           void *y, void *h, float *post_stats, float *pre_stats, void *stream);
+
+/*
+ * Backward.  dy: gradient to y from everything after it but h (NULL: zero; with pre
+ * CBR_NORM_NONE it is needed); dh: gradient to h.  With vhat the normalised values,
+ *   D  = dy + (pre norm's backward of dh at y):  dx = D                    stream (out)
+ *   dg_ic = alpha r_c sum_{rows of i} D n,   dr_c = alpha sum D g n
+ *   df = post norm's backward of alpha r g D,                               branch (out)
+ *   dpost_w = sum alpha r g D nhat,  dpost_b = sum alpha r g D,
+ *   dpre_w = sum dh yhat,            dpre_b = sum dh
+ * y, f, post_stats, pre_stats as the forward left them (y: x where f is NULL; y and
+ * pre_stats are read only for a pre norm, post_stats only for a post norm).  Without f
+ * the branch outputs are NULL and dx is the gradient to x.
+ * dpost_w, dpost_b, dgate, dres_scale, dpre_w, dpre_b may each be NULL (not wanted); a
+ * gradient of something that has no value here is refused (CBR_E_VALUE), but dpost_b and
+ * dpre_b need no bias, dpost_w and dpre_w no weight and dres_scale no res_scale: where the
+ * forward read 1 or 0 the gradient exists all the same.
+ * The sums over rows run in a fixed order: fp32 over a workgroup's rows, then fp64.
+ * dx may alias dy and df may alias f or dh (same type and place).
+ */
+int cbr_block_norm_backward(const cbr_block_shape *shape, const void *dy, const void *dh,
+                            const void *y, const void *f,
+                            const float *post_w, const float *post_b, const void *gate,
+                            const float *res_scale, const float *pre_w,
+                            const float *post_stats, const float *pre_stats,
+                            void *dx, void *df, float *dpost_w, float *dpost_b, void *dgate,
+                            float *dres_scale, float *dpre_w, float *dpre_b,
+                            void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * 8-bit floating point: operands with a scale for each block of 128
+ * ------------------------------------------------------------------
+ * src [rows][cols], dense, of CBR_BF16, CBR_F16 or CBR_F32; v is src, or its transpose
+ * where `transpose` is non-zero, with v_rows rows of v_cols values.  v is written in
+ * q_type (CBR_E4M3: finite values up to 448; CBR_E5M2: up to 57344) with one scale for
+ * each group of `block` rows by 128 columns of v (block 1 or 128), groups at the edges
+ * being smaller:
+ *   a = max(largest |v| of the group, fmax * 2^-126),  scale = a / fmax,
+ *   q = v * fmax / a, rounded to nearest, ties to even: v = q * scale up to rounding.
+ * q [v_rows][ldq] bytes, ldq >= v_cols a multiple of 16; bytes past v_cols of a row are
+ * left as they are.  scale: float [ceil(v_cols / 128)][ceil(v_rows / block)], the blocks
+ * of 128 columns outermost.  A NaN becomes NaN and does not touch the rest of its group;
+ * an infinity makes its group's scale infinite, and the group stands for NaN.
+ * rows and cols positive, < 2^31, and fewer than 2^31 groups of 16 rows by 128 columns.
+ */
+typedef struct cbr_quant_shape {
+    int64_t rows, cols;             /* of src                                         */
+    int64_t ldq;                    /* bytes from a row of q to the next              */
+    int32_t src_type, q_type;       /* enum cbr_dtype                                 */
+    int32_t transpose, block;
+} cbr_quant_shape;
+
+int cbr_fp8_quantize(const cbr_quant_shape *shape, const void *src, void *q, float *scale, void *stream);
+
+/*
+ * Matrix product of such operands (a 1x1 convolution's forward, data gradient or weight
+ * gradient over N*H*W pixels):
+ *   d[i][j] = act( sum_t a_scale[t][i] * b_scale[t][j / b_block]
+ *                        * sum_{k in block t} a[i][k] * b[j][k]  + bias[j] )
+ * a [m][lda], b [n][ldb] bytes in a_type, b_type (CBR_E4M3 or CBR_E5M2), row strides
+ * multiples of 16 and at least k; what lies past k in a row is not used.  a_scale
+ * [ceil(k/128)][m] (block 1), b_scale [ceil(k/128)][ceil(n / b_block)], b_block 1 or 128.
+ * d [m][n] dense, d_type CBR_BF16, CBR_F16 or CBR_F32; bias float [n] or NULL; act is
+ * max(v, 0) where relu is non-zero (a NaN stays one), else v.  Blocks are scaled and added
+ * in fp32.  Within a block the sums are fp32 too for d_type CBR_F32 and for m <= 64; for
+ * 16-bit outputs of more rows the 8-bit matrix instruction sums each eight consecutive
+ * products with 13 bits below the leading one of the largest (about 1.3e-5 of the result's
+ * norm), and everything beyond the eight in fp32.
+ *   forward:          a = activations [pixels][C], b = filter [K][C] with b_block 128
+ *   data gradient:    a = dy [pixels][K],          b = filter transposed [C][K], b_block 128
+ *   weight gradient:  a = dy transposed [K][pixels], b = activations transposed, b_block 1
+ * m, n, k positive; m < 2^31, n, lda, ldb <= 2^23 (CBR_E_UNSUPPORTED beyond that); a
+ * stride that is too small or no multiple of 16 is CBR_E_SHAPE.
+ * The workspace (cbr_gemm_fp8_workspace_bytes, 0 where the shape needs none or is
+ * invalid) holds the parts of a long sum that several workgroups share; they are added in
+ * a fixed order.
+ */
+typedef struct cbr_gemm_shape {
+    int64_t m;
+    int64_t n, k;
+    int64_t lda, ldb;               /* bytes from a row to the next                   */
+    int32_t a_type, b_type, d_type; /* enum cbr_dtype                                 */
+    int32_t b_block;                /* 1 or 128                                       */
+    int32_t relu;
+} cbr_gemm_shape;
+
+size_t cbr_gemm_fp8_workspace_bytes(const cbr_gemm_shape *shape);
+
+int cbr_gemm_fp8(const cbr_gemm_shape *shape, const void *a, const float *a_scale, const void *b,
+                 const float *b_scale, const float *bias, void *d,
+                 void *workspace, size_t ws_bytes, void *stream);
 
 /*
  * Kernel plans (tuning interface).  Each convolution stage of a call runs one kernel and

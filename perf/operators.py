@@ -350,7 +350,8 @@ def _own_quantize(cbr, st):
     rows, cols = (st["cols"], st["rows"]) if st["transpose"] else (st["rows"], st["cols"])
     dt = {"bf16": cbr.CBR_BF16, "f16": cbr.CBR_F16, "f32": cbr.CBR_F32, "e4m3": cbr.CBR_E4M3, "e5m2": cbr.CBR_E5M2}
     if "sp" not in st:
-        st["sp"] = cbr.make_quant_shape(st["rows"], st["cols"], src_type=dt[st["src"]], q_type=dt[st["fmt"]],
+        src = {v: dt[k] for k, v in TYPES.items()}[st["src"].dtype]
+        st["sp"] = cbr.make_quant_shape(st["rows"], st["cols"], src_type=src, q_type=dt[st["fmt"]],
                                         transpose=st["transpose"], block=st["block"])
     q = torch.empty(rows, _cdiv(cols, 16) * 16, dtype=TYPES[st["fmt"]], device=st["src"].device)
     s = torch.empty(_cdiv(cols, BLK), _cdiv(rows, st["block"]), device=st["src"].device)

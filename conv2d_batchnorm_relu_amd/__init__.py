@@ -308,44 +308,61 @@ def cbr_conv2d_bias(shape, x, w, bias, y, stream=None, events=None):
 
 
 # Element types that a tensor of each cbr_dtype may have: its own, or an integer of its size.
-_DTYPES = {CBR_BF16: ("torch.bfloat16", "torch.int16", "torch.uint16"), CBR_F16: ("torch.float16", "torch.int16", "torch.uint16"),
-           CBR_F32: ("torch.float32",), CBR_E4M3: ("torch.float8_e4m3fn", "torch.uint8", "torch.int8"),
-           CBR_E5M2: ("torch.float8_e5m2", "torch.uint8", "torch.int8")}
-_dtypes = None   # the same as sets of torch's own, made on the first call
+_DTYPES = {CBR_BF16: ("bfloat16", "int16", "uint16"), CBR_F16: ("float16", "int16", "uint16"),
+           CBR_F32: ("float32",), CBR_E4M3: ("float8_e4m3fn", "uint8", "int8"),
+           CBR_E5M2: ("float8_e5m2", "uint8", "int8")}
 
 
-def _arg(t, kind, name, where, numel=None):
-    """Device address of tensor t of cbr_dtype kind, after _ptr's checks and two more: the
-    tensor's own type is that type, and it lives on the current device (the one whose stream
-    the call runs on)."""
-    global _dtypes
-    if t is None or isinstance(t, int):
-        return t
-    import torch
-    if _dtypes is None:
-        _dtypes = {k: frozenset(getattr(torch, n[6:]) for n in v) for k, v in _DTYPES.items()}
-    p = _ptr(t, _BYTES[kind], name, where, numel)
-    if t.dtype not in _dtypes[kind]:
-        raise CbrError(_E_VALUE, where, f"{name} is {t.dtype}, expected {_DTYPES[kind][0]}")
-    if t.get_device() != torch.cuda.current_device():
-        raise CbrError(_E_VALUE, where, f"{name} is on GPU {t.get_device()}, the current one is "
-                                        f"{torch.cuda.current_device()}")
-    return p
+class _Call:
+    """One call's view of its tensors: the current device (the one whose stream it runs on) and
+    the checks.  These run for every tensor of every call, a dozen of them beside a kernel of a
+    few microseconds, so the accepted case is one line; only a refused tensor is looked at
+    again to say why."""
+    types = None   # cbr_dtype -> frozenset of torch types, made on the first call
 
+    def __init__(self, where, *kinds):
+        import torch
+        if _Call.types is None:
+            _Call.types = {k: frozenset(getattr(torch, n) for n in v) for k, v in _DTYPES.items()}
+        for k in kinds:
+            if k not in _BYTES:
+                raise CbrError(_E_VALUE, where)
+        self.where = where
+        self.torch = torch
+        self.dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
 
-def _work(workspace, where):
-    """_ws for a workspace on the current device; None where there is none."""
-    if workspace is None or isinstance(workspace, tuple):
-        return _ws(workspace, where)
-    import torch
-    if workspace.is_cuda and workspace.get_device() != torch.cuda.current_device():
-        raise CbrError(_E_VALUE, where, "workspace is not on the current GPU")
-    return _ws(workspace, where)
+    def at(self, t, kind, name, numel):
+        """Device address of tensor t of cbr_dtype kind with numel elements at least (None: not
+        known).  None stays NULL, an integer is taken as an address."""
+        if t is None:
+            return None
+        if type(t) is int:
+            return t
+        if (t.dtype in _Call.types[kind] and t.get_device() == self.dev and t.is_contiguous()
+                and (numel is None or t.numel() >= numel)):
+            return t.data_ptr()
+        p = _ptr(t, _BYTES[kind], name, self.where, numel)
+        if t.dtype not in _Call.types[kind]:
+            raise CbrError(_E_VALUE, self.where, f"{name} is {t.dtype}, expected torch.{_DTYPES[kind][0]}")
+        if t.get_device() != self.torch.cuda.current_device():
+            raise CbrError(_E_VALUE, self.where, f"{name} is on GPU {t.get_device()}, the current one is "
+                                                 f"{self.torch.cuda.current_device()}")
+        return p
 
+    def stream(self, stream):
+        """The stream's handle (None: the current one, without the Stream object that
+        torch.cuda.current_stream() makes: 2.8 us a call against 0.1)."""
+        if stream is None:
+            return self.torch._C._cuda_getCurrentRawStream(self.torch.cuda.current_device())
+        return _stream(stream)
 
-def _kinds(where, *kinds):
-    if any(k not in _BYTES for k in kinds):
-        raise CbrError(_E_VALUE, where)
+    def workspace(self, workspace):
+        """Address and bytes of a workspace (None: none; a pair is taken as they are)."""
+        if workspace is None or isinstance(workspace, tuple):
+            return _ws(workspace, self.where)
+        if workspace.is_cuda and workspace.get_device() != self.torch.cuda.current_device():
+            raise CbrError(_E_VALUE, self.where, "workspace is not on the current GPU")
+        return _ws(workspace, self.where)
 
 
 def make_block_shape(rows, channels, rows_per_gate=0, post=CBR_NORM_NONE, pre=CBR_NORM_NONE, stream_type=CBR_BF16,
@@ -361,36 +378,37 @@ def cbr_block_norm_forward(shape, x, f, post_w, post_b, gate, res_scale, pre_w, 
                            pre_stats=None, stream=None):
     """y = x + alpha * res_scale * gate * post(f) and h = pre(y), as include/cbr.h describes;
     None is a pointer that is not given."""
-    w, s = "cbr_block_norm_forward", shape
+    s = shape
     S, B, F = s.stream_type, s.branch_type, CBR_F32
-    _kinds(w, S, B)
-    n, c, st = s.rows * s.channels, s.channels, 2 * s.rows
+    call = _Call("cbr_block_norm_forward", S, B)
+    at, c = call.at, s.channels
+    n, st = s.rows * c, 2 * s.rows
     g = s.rows // s.rows_per_gate * c if s.rows_per_gate > 0 else None
     _check(_load().cbr_block_norm_forward(
-        _sp(s), _arg(x, S, "x", w, n), _arg(f, B, "f", w, n), _arg(post_w, F, "post_w", w, c),
-        _arg(post_b, F, "post_b", w, c), _arg(gate, B, "gate", w, g), _arg(res_scale, F, "res_scale", w, c),
-        _arg(pre_w, F, "pre_w", w, c), _arg(pre_b, F, "pre_b", w, c), _arg(y, S, "y", w, n), _arg(h, B, "h", w, n),
-        _arg(post_stats, F, "post_stats", w, st), _arg(pre_stats, F, "pre_stats", w, st), _stream(stream)), w)
+        _sp(s), at(x, S, "x", n), at(f, B, "f", n), at(post_w, F, "post_w", c), at(post_b, F, "post_b", c),
+        at(gate, B, "gate", g), at(res_scale, F, "res_scale", c), at(pre_w, F, "pre_w", c), at(pre_b, F, "pre_b", c),
+        at(y, S, "y", n), at(h, B, "h", n), at(post_stats, F, "post_stats", st), at(pre_stats, F, "pre_stats", st),
+        call.stream(stream)), call.where)
 
 
 def cbr_block_norm_backward(shape, dy, dh, y, f, post_w, post_b, gate, res_scale, pre_w, post_stats, pre_stats, dx, df,
                             dpost_w, dpost_b, dgate, dres_scale, dpre_w, dpre_b, workspace, stream=None):
     """Gradients of cbr_block_norm_forward; None is a pointer that is not given (a gradient
     that is not wanted)."""
-    w, s = "cbr_block_norm_backward", shape
+    s = shape
     S, B, F = s.stream_type, s.branch_type, CBR_F32
-    _kinds(w, S, B)
-    n, c, st = s.rows * s.channels, s.channels, 2 * s.rows
+    call = _Call("cbr_block_norm_backward", S, B)
+    at, c = call.at, s.channels
+    n, st = s.rows * c, 2 * s.rows
     g = s.rows // s.rows_per_gate * c if s.rows_per_gate > 0 else None
-    ws, nbytes = _work(workspace, w)
+    ws, nbytes = call.workspace(workspace)
     _check(_load().cbr_block_norm_backward(
-        _sp(s), _arg(dy, S, "dy", w, n), _arg(dh, B, "dh", w, n), _arg(y, S, "y", w, n), _arg(f, B, "f", w, n),
-        _arg(post_w, F, "post_w", w, c), _arg(post_b, F, "post_b", w, c), _arg(gate, B, "gate", w, g),
-        _arg(res_scale, F, "res_scale", w, c), _arg(pre_w, F, "pre_w", w, c),
-        _arg(post_stats, F, "post_stats", w, st), _arg(pre_stats, F, "pre_stats", w, st), _arg(dx, S, "dx", w, n),
-        _arg(df, B, "df", w, n), _arg(dpost_w, F, "dpost_w", w, c), _arg(dpost_b, F, "dpost_b", w, c),
-        _arg(dgate, B, "dgate", w, g), _arg(dres_scale, F, "dres_scale", w, c), _arg(dpre_w, F, "dpre_w", w, c),
-        _arg(dpre_b, F, "dpre_b", w, c), ws, nbytes, _stream(stream)), w)
+        _sp(s), at(dy, S, "dy", n), at(dh, B, "dh", n), at(y, S, "y", n), at(f, B, "f", n), at(post_w, F, "post_w", c),
+        at(post_b, F, "post_b", c), at(gate, B, "gate", g), at(res_scale, F, "res_scale", c), at(pre_w, F, "pre_w", c),
+        at(post_stats, F, "post_stats", st), at(pre_stats, F, "pre_stats", st), at(dx, S, "dx", n), at(df, B, "df", n),
+        at(dpost_w, F, "dpost_w", c), at(dpost_b, F, "dpost_b", c), at(dgate, B, "dgate", g),
+        at(dres_scale, F, "dres_scale", c), at(dpre_w, F, "dpre_w", c), at(dpre_b, F, "dpre_b", c), ws, nbytes,
+        call.stream(stream)), call.where)
 
 
 def make_quant_shape(rows, cols, src_type=CBR_BF16, q_type=CBR_E4M3, transpose=False, block=1,
@@ -403,15 +421,15 @@ def make_quant_shape(rows, cols, src_type=CBR_BF16, q_type=CBR_E4M3, transpose=F
 
 def cbr_fp8_quantize(shape, src, q, scale, stream=None):
     """src (or its transpose) in 8 bits, q [rows][ldq] bytes, with its scales (include/cbr.h)."""
-    w, s = "cbr_fp8_quantize", shape
-    _kinds(w, s.src_type, s.q_type)
+    s = shape
+    call = _Call("cbr_fp8_quantize", s.src_type, s.q_type)
     if s.block not in (1, 128):
-        raise CbrError(_E_VALUE, w)
+        raise CbrError(_E_VALUE, call.where)
     rows, cols = (s.cols, s.rows) if s.transpose else (s.rows, s.cols)
-    _check(_load().cbr_fp8_quantize(_sp(s), _arg(src, s.src_type, "src", w, s.rows * s.cols),
-                                    _arg(q, s.q_type, "q", w, (rows - 1) * s.ldq + cols),
-                                    _arg(scale, CBR_F32, "scale", w, -(-cols // 128) * -(-rows // s.block)),
-                                    _stream(stream)), w)
+    _check(_load().cbr_fp8_quantize(_sp(s), call.at(src, s.src_type, "src", s.rows * s.cols),
+                                    call.at(q, s.q_type, "q", (rows - 1) * s.ldq + cols),
+                                    call.at(scale, CBR_F32, "scale", -(-cols // 128) * -(-rows // s.block)),
+                                    call.stream(stream)), call.where)
 
 
 def make_gemm_shape(m, n, k, a_type=CBR_E4M3, b_type=CBR_E4M3, d_type=CBR_BF16, b_block=128, relu=False, lda=None,
@@ -429,15 +447,14 @@ def cbr_gemm_fp8_workspace_bytes(shape: CbrGemmShape) -> int:
 def cbr_gemm_fp8(shape, a, a_scale, b, b_scale, bias, d, workspace=None, stream=None):
     """d = act((a * a_scale) (b * b_scale)^T + bias) of 8-bit operands (include/cbr.h); workspace
     may be None where cbr_gemm_fp8_workspace_bytes is 0."""
-    w, s = "cbr_gemm_fp8", shape
-    _kinds(w, s.a_type, s.b_type, s.d_type)
+    s = shape
+    call = _Call("cbr_gemm_fp8", s.a_type, s.b_type, s.d_type)
     if s.b_block not in (1, 128):
-        raise CbrError(_E_VALUE, w)
-    kb = -(-s.k // 128)
-    ws, nbytes = _work(workspace, w)
-    _check(_load().cbr_gemm_fp8(_sp(s), _arg(a, s.a_type, "a", w, s.m * s.lda),
-                                _arg(a_scale, CBR_F32, "a_scale", w, kb * s.m),
-                                _arg(b, s.b_type, "b", w, s.n * s.ldb),
-                                _arg(b_scale, CBR_F32, "b_scale", w, kb * -(-s.n // s.b_block)),
-                                _arg(bias, CBR_F32, "bias", w, s.n), _arg(d, s.d_type, "d", w, s.m * s.n),
-                                ws, nbytes, _stream(stream)), w)
+        raise CbrError(_E_VALUE, call.where)
+    m, n, kb, at = s.m, s.n, -(-s.k // 128), call.at
+    ws, nbytes = call.workspace(workspace)
+    _check(_load().cbr_gemm_fp8(_sp(s), at(a, s.a_type, "a", m * s.lda), at(a_scale, CBR_F32, "a_scale", kb * m),
+                                at(b, s.b_type, "b", n * s.ldb),
+                                at(b_scale, CBR_F32, "b_scale", kb * -(-n // s.b_block)),
+                                at(bias, CBR_F32, "bias", n), at(d, s.d_type, "d", m * n), ws, nbytes,
+                                call.stream(stream)), call.where)

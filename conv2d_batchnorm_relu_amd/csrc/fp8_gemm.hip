@@ -41,7 +41,7 @@ struct GemmArgs {
     int kb_per;         // blocks of k a split takes
     int sb_ld;          // scales of b in a block of k
     int d_type, relu;
-    int tiles_m, tiles_n;
+    int tiles_m, tiles_n, splits;
 };
 
 struct __attribute__((packed, aligned(2))) Loose8 {
@@ -133,10 +133,38 @@ __device__ __forceinline__ void vm_wait()
 {
     asm volatile("s_waitcnt vmcnt(%0)" : : "i"(N) : "memory");
 }
-__device__ __forceinline__ void after_wait(u32x4 &x) { asm volatile("" : "+v"(x)); }
+// "At most min(n, MOST) stages of PER loads outstanding."
+template <int PER, int MOST>
+__device__ __forceinline__ void vm_wait_stages(int n)
+{
+    if constexpr (MOST == 0) {
+        vm_wait<0>();
+    } else {
+        if (n >= MOST) vm_wait<PER * MOST>();
+        else vm_wait_stages<PER, MOST - 1>(n);
+    }
+}
+// Ties a register to the wait before it, so that its use stays behind the wait.
+template <typename T>
+__device__ __forceinline__ void after_wait(T &x)
+{
+    asm volatile("" : "+v"(x));
+}
+template <int OFF>
+__device__ __forceinline__ float lds_read4(uint32_t addr)
+{
+    float v;
+    asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFF) : "memory");
+    return v;
+}
+// 16 or 4 bytes per lane from buffer offset voff to LDS dst + that times lane (zeros past the end).
 __device__ __forceinline__ void buffer_load_lds16(__amdgpu_buffer_rsrc_t r, lds_u8 *dst, int voff)
 {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, voff, 0, 0, 0);
+}
+__device__ __forceinline__ void buffer_load_lds4(__amdgpu_buffer_rsrc_t r, lds_u8 *dst, int voff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 4, voff, 0, 0, 0);
 }
 
 // Four results of consecutive n at (m, n): bias, activation, rounding, store.
@@ -171,10 +199,10 @@ __device__ __forceinline__ void finish4(const GemmArgs &p, int64_t m, int n, f32
             if (e < left) o[e] = (uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
 }
 
-__device__ __forceinline__ void emit4(const GemmArgs &p, int64_t m, int n, f32x4 v)
+__device__ __forceinline__ void emit4(const GemmArgs &p, int split, int64_t m, int n, f32x4 v)
 {
     if (p.part) {
-        float *o = p.part + ((int64_t)blockIdx.y * p.M + m) * p.N + n;
+        float *o = p.part + ((int64_t)split * p.M + m) * p.N + n;
         if (n + 4 <= p.N) ((LooseF4 *)o)->v = v;
         else
             for (int e = 0; e < 3; ++e)
@@ -196,18 +224,47 @@ __device__ __forceinline__ f32x4 scale4(const GemmArgs &p, int kb, int n)
     return v;
 }
 
+// Workgroup -> tile and split.  Workgroups go to the eight XCDs in turn, each with its own L2.
+// Where k is shared out, an XCD takes whole splits (all tiles of them: the operands' columns
+// of a split are then fetched once; splits are a multiple of 8 where there are that many).
+// Otherwise it takes an eighth of the tiles, in groups of 8 rows of tiles walked down first,
+// so that the tiles that run together share rows of both operands.
+__device__ __forceinline__ void place(const GemmArgs &p, int &tm, int &tn, int &split)
+{
+    const uint32_t id = blockIdx.x;
+    uint32_t t;
+    if (p.splits > 1) {
+        split = id % p.splits;
+        t = id / p.splits;
+    } else {
+        const uint32_t all = gridDim.x, x = id % 8, q = all / 8, r = all % 8;
+        split = 0;
+        t = x * q + min(x, r) + id / 8;
+    }
+    const uint32_t per = 8u * p.tiles_n, first = t / per * 8, rows = min(8u, p.tiles_m - first);
+    t %= per;
+    tm = first + t % rows;
+    tn = t / rows;
+}
+
 // Tile kernel: 16 MS WM x 16 NS WN results a workgroup, WM x WN waves of 16 MS x 16 NS.
-// Both operands' rows of a k block (128 bytes) come straight into LDS, two blocks deep:
-// block t + 1 loads while block t is multiplied.  16-byte chunk c of row r lies at
-// c ^ ((r / 2) % 8), so the sixteen rows of a fragment read fall on all 64 banks.
-// WIDE: through bf16.
-template <int MS, int NS, int WM, int WN, int FA, int FB, int BB, bool WIDE>
+// Both operands' rows of a k block (128 bytes) and their scales come straight into LDS, NST
+// blocks deep: while block t is multiplied, blocks t + 1 .. t + NST - 1 are on their way, and
+// a wave waits for its own loads of a block by their count, then for the other waves at the
+// one barrier a block.  16-byte chunk c of row r lies at c ^ ((r / 2) % 8), so the sixteen
+// rows of a fragment read fall on all 64 banks.  WIDE: through bf16.
+template <int BM, int BN>
+constexpr int stage_bytes() { return (BM + BN) * BK + (BM + BN) * 4; }   // rows, then scales
+
+template <int MS, int NS, int WM, int WN, int NST, int FA, int FB, int BB, bool WIDE>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
 {
     constexpr int NW = WM * WN, BM = 16 * MS * WM, BN = 16 * NS * WN;
     constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;   // load instructions a wave, 8 rows each
-    constexpr int STAGE = (BM + BN) * BK;
+    constexpr int PER = LA + LB + 2;                    // and two for the scales
+    constexpr int STAGE = stage_bytes<BM, BN>(), SCALES = (BM + BN) * BK;
     static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN && NW >= 2, "tile shape");
+    static_assert(64 * NW % BM == 0 && 64 * NW % BN == 0, "a scale's loads cover the tile evenly");
     static_assert(BB == 1 || 128 % (16 * NS) == 0, "a wave's columns lie in one block of b");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const uint32_t lbase = (uint32_t)(uintptr_t)(lds_u8 *)lds;
@@ -215,10 +272,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
     const int r16 = lane & 15, g = lane >> 4;
     const int wm = wave / WN, wn = wave % WN;
 
-    const int tm = blockIdx.x % p.tiles_m, tn = blockIdx.x / p.tiles_m;
+    int tm, tn, split;
+    place(p, tm, tn, split);
     const int64_t m0 = (int64_t)tm * BM;
     const int n0 = tn * BN;
-    const int kb0 = blockIdx.y * p.kb_per, kb1 = min(p.kbs, kb0 + p.kb_per);
+    const int kb0 = split * p.kb_per, kb1 = min(p.kbs, kb0 + p.kb_per);
 
     // rows past the end of an operand lie past the end of its buffer and read as zeros
     const int rows_a = (int)min((int64_t)BM, p.M - m0), rows_b = min(BN, p.N - n0);
@@ -228,34 +286,26 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         __builtin_amdgcn_make_buffer_rsrc((void *)(p.b + (int64_t)n0 * p.ldb), 0, rows_b * p.ldb, 0x00020000);
     const int lrow = 8 * wave + (lane >> 3);
     const int lchunk = 16 * ((lane & 7) ^ ((lrow >> 1) & 7));
-    auto load = [&](int kb) __attribute__((always_inline)) {
+    const int sa_at = wave * 64 % BM, sb_at = wave * 64 % BN;
+    const int sb_n = BB == 1 ? rows_b : (rows_b + 127) / 128;
+    auto load = [&](int kb, int st) __attribute__((always_inline)) {
         const int kat = kb * BK + lchunk;
         const bool in = kat < p.K;   // a chunk past K is not read: zeros
-        lds_u8 *dst = (lds_u8 *)lds + (kb & 1) * STAGE + wave * 1024;
+        lds_u8 *base = (lds_u8 *)lds + st * STAGE;
+        lds_u8 *dst = base + wave * 1024;
 #pragma unroll
         for (int t = 0; t < LA; ++t)
             buffer_load_lds16(ra, dst + t * NW * 1024, in ? (lrow + t * 8 * NW) * p.lda + kat : (int)OOB);
 #pragma unroll
         for (int t = 0; t < LB; ++t)
             buffer_load_lds16(rb, dst + BM * BK + t * NW * 1024, in ? (lrow + t * 8 * NW) * p.ldb + kat : (int)OOB);
-    };
-
-    // this lane's rows of a and columns of b
-    const int64_t mw = m0 + wm * 16 * MS + r16;
-    const int nw = n0 + wn * 16 * NS;
-    const int nl = nw + 4 * g;
-    float sa[MS];
-    f32x4 sb[BB == 1 ? NS : 1];
-    auto scales = [&](int kb) __attribute__((always_inline)) {
-        const float *s = p.sa + (int64_t)kb * p.M;
-#pragma unroll
-        for (int j = 0; j < MS; ++j) sa[j] = s[min(mw + 16 * j, p.M - 1)];
-        if constexpr (BB == 1) {
-#pragma unroll
-            for (int i = 0; i < NS; ++i) sb[i] = scale4(p, kb, nl + 16 * i);
-        } else {
-            sb[0][0] = p.sb[(int64_t)kb * p.sb_ld + min(nw, p.N - 1) / 128];
-        }
+        // 64 scales a wave; where there are more waves than that, several load the same ones
+        const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)(p.sa + (int64_t)kb * p.M + m0), 0, rows_a * 4, 0x00020000);
+        const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)(p.sb + (int64_t)kb * p.sb_ld + n0 / BB), 0, sb_n * 4, 0x00020000);
+        buffer_load_lds4(rsa, base + SCALES + sa_at * 4, (sa_at + lane) * 4);
+        buffer_load_lds4(rsb, base + SCALES + BM * 4 + sb_at * 4, (sb_at + lane) * 4);
     };
 
     f32x4 acc[NS][MS];
@@ -264,21 +314,31 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
 #pragma unroll
         for (int j = 0; j < MS; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const uint32_t fa0 = lbase + (wm * 16 * MS + r16) * BK + 16 * (g ^ ((r16 >> 1) & 7));
-    const uint32_t fb0 = lbase + BM * BK + (wn * 16 * NS + r16) * BK + 16 * (g ^ ((r16 >> 1) & 7));
+    const int frag = r16 * BK + 16 * (g ^ ((r16 >> 1) & 7));
+    const uint32_t fa0 = lbase + wm * 16 * MS * BK + frag;
+    const uint32_t fb0 = lbase + (BM + wn * 16 * NS) * BK + frag;
+    const uint32_t sa0 = lbase + SCALES + (wm * 16 * MS + r16) * 4;
+    const uint32_t sb0 = lbase + SCALES + BM * 4 + (BB == 1 ? wn * 16 * NS + 4 * g : wn * 16 * NS / 128) * 4;
 
-    load(kb0);
-    scales(kb0);
-    for (int kb = kb0; kb < kb1; ++kb) {
-        vm_wait<0>();
+    const int turns = kb1 - kb0;
+#pragma unroll
+    for (int t = 0; t < NST - 1; ++t)
+        if (t < turns) load(kb0 + t, t);
+    int st = 0;
+    for (int t = 0; t < turns; ++t) {
+        vm_wait_stages<PER, NST - 2>(turns - 1 - t);
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
+        const int kb = kb0 + t;
+        // Block t + NST - 1 takes the place of block t - 1: every wave is past its reads (their
+        // values went into products) when it reaches the barrier.
+        if (t + NST - 1 < turns) load(kb + NST - 1, st == 0 ? NST - 1 : st - 1);
         if (kb + 1 == p.kbs && (p.K & 15)) {
-            // the chunk that K ends in: clear what lies past it (block b of 128 ends at K)
+            // the chunk that K ends in: clear what lies past it
             const int kl = p.K - kb * BK, c = kl >> 4, cut = kl & 15;
             for (int r = threadIdx.x; r < BM + BN; r += 64 * NW) {
-                u32x4 *q = (u32x4 *)(lds + (kb & 1) * STAGE + r * BK + 16 * (c ^ ((r >> 1) & 7)));
+                u32x4 *q = (u32x4 *)(lds + st * STAGE + r * BK + 16 * (c ^ ((r >> 1) & 7)));
                 u32x4 v = *q;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -289,29 +349,32 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
             }
             __syncthreads();
         }
-        float s[MS];
+        const uint32_t fa = fa0 + st * STAGE, fb = fb0 + st * STAGE;
+        const uint32_t fax = fa ^ 64, fbx = fb ^ 64;
+        float s[MS], s1;
         f32x4 t4[BB == 1 ? NS : 1];
-#pragma unroll
-        for (int j = 0; j < MS; ++j) s[j] = BB == 1 ? sa[j] : sa[j] * sb[0][0];
+        unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
+            constexpr int j = decltype(jc)::value;
+            s[j] = lds_read4<j * 64>(sa0 + st * STAGE);
+        });
         if constexpr (BB == 1)
-#pragma unroll
-            for (int i = 0; i < NS; ++i) t4[i] = sb[i];
-        if (kb + 1 < kb1) {
-            scales(kb + 1);
-            load(kb + 1);
-        }
-        const uint32_t fa = fa0 + (kb & 1) * STAGE, fb = fb0 + (kb & 1) * STAGE;
+            unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
+                constexpr int i = decltype(ic)::value;
+                t4[i] = __builtin_bit_cast(f32x4, lds_read16<i * 64>(sb0 + st * STAGE));
+            });
+        else
+            s1 = lds_read4<0>(sb0 + st * STAGE);
         u32x4 bf[NS][2], af[3][2];
         unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
             constexpr int i = decltype(ic)::value;
             bf[i][0] = lds_read16<i * 16 * BK>(fb);
-            bf[i][1] = lds_read16<i * 16 * BK>(fb ^ 64);
+            bf[i][1] = lds_read16<i * 16 * BK>(fbx);
         });
         af[0][0] = lds_read16<0>(fa);
-        af[0][1] = lds_read16<0>(fa ^ 64);
+        af[0][1] = lds_read16<0>(fax);
         if constexpr (MS > 1) {
             af[1][0] = lds_read16<16 * BK>(fa);
-            af[1][1] = lds_read16<16 * BK>(fa ^ 64);
+            af[1][1] = lds_read16<16 * BK>(fax);
         }
         f32x4 q[NS];
         Wide<FB> wb[WIDE ? NS : 1];
@@ -323,24 +386,39 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
             constexpr int J = decltype(jc)::value;
             lgkm_wait<(J + 1 < MS ? 2 : 0)>();   // all but the next fragment of a
-            if constexpr (J == 0)
+            if constexpr (J == 0) {
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
                     after_wait(bf[i][0]);
                     after_wait(bf[i][1]);
                 }
+#pragma unroll
+                for (int j = 0; j < MS; ++j) after_wait(s[j]);
+                if constexpr (BB == 1) {
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) after_wait(t4[i]);
+                } else {
+                    after_wait(s1);
+#pragma unroll
+                    for (int j = 0; j < MS; ++j) s[j] *= s1;
+                }
+            }
             after_wait(af[J % 3][0]);
             after_wait(af[J % 3][1]);
-            if constexpr (J + 2 < MS) {
-                af[(J + 2) % 3][0] = lds_read16<(J + 2) * 16 * BK>(fa);
-                af[(J + 2) % 3][1] = lds_read16<(J + 2) * 16 * BK>(fa ^ 64);
-            }
+            // the next fragment but one, once the products that read its registers are under way
+            auto ahead = [&]() __attribute__((always_inline)) {
+                if constexpr (J + 2 < MS) {
+                    af[(J + 2) % 3][0] = lds_read16<(J + 2) * 16 * BK>(fa);
+                    af[(J + 2) % 3][1] = lds_read16<(J + 2) * 16 * BK>(fax);
+                }
+            };
             if constexpr (WIDE) {
                 if constexpr (J == 0)
 #pragma unroll
                     for (int i = 0; i < NS; ++i) wb[i].set(bf[i][0], bf[i][1]);
                 Wide<FA> wa;
                 wa.set(af[J % 3][0], af[J % 3][1]);
+                ahead();
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -354,21 +432,71 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
                 for (int i = 0; i < NS; ++i) {
                     if constexpr (J > 0) add(i, J - 1);
                     q[i] = product<FB, FA>(join(bf[i][0], bf[i][1]), av);
+                    if (i == 0) ahead();
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         });
 #pragma unroll
         for (int i = 0; i < NS; ++i) add(i, MS - 1);
-        // every wave has read this block before block kb + 2 overwrites it: the barrier of
-        // the next turn, which this wave reaches with its reads done (the products used them)
+        st = st + 1 == NST ? 0 : st + 1;
     }
+    // Epilogue: bias (0 without one) and activation (a lower bound: 0, or none), then whole
+    // quads, or value by value in a tile that N ends in.
+    const int nl = n0 + wn * 16 * NS + 4 * g;
+    const int64_t mw = m0 + wm * 16 * MS + r16;
+    const bool whole = n0 + BN <= p.N, half = p.d_type == CBR_F16;
+    const float *bias = p.part ? nullptr : p.bias;
+    const float low = p.relu && !p.part ? 0.f : -__builtin_inff();
+    f32x4 bv[NS];
 #pragma unroll
-    for (int j = 0; j < MS; ++j) {
-        const int64_t m = mw + 16 * j;
-        if (m >= p.M) continue;
+    for (int i = 0; i < NS; ++i) {
+        bv[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (bias) {
+            if (whole) bv[i] = *(const f32x4 *)(bias + nl + 16 * i);
+            else
 #pragma unroll
-        for (int i = 0; i < NS; ++i)
-            if (nl + 16 * i < p.N) emit4(p, m, nl + 16 * i, acc[i][j]);
+                for (int e = 0; e < 4; ++e)
+                    if (nl + 16 * i + e < p.N) bv[i][e] = bias[nl + 16 * i + e];
+        }
+    }
+    auto value = [&](int i, int j) __attribute__((always_inline)) {
+        f32x4 v = acc[i][j] + bv[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = v[e] < low ? low : v[e];   // a NaN stays one
+        return v;
+    };
+    const int64_t step = 16 * (int64_t)p.N;
+    if (WIDE || p.part) {   // fp32
+        float *o = (p.part ? p.part + (int64_t)split * p.M * p.N : (float *)p.d) + mw * p.N + nl;
+#pragma unroll
+        for (int j = 0; j < MS; ++j, o += step)
+            if (mw + 16 * j < p.M)
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    const f32x4 v = value(i, j);
+                    if (whole) ((LooseF4 *)(o + 16 * i))->v = v;
+                    else
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (nl + 16 * i + e < p.N) o[16 * i + e] = v[e];
+                }
+    } else {
+        uint16_t *o = (uint16_t *)p.d + mw * p.N + nl;
+#pragma unroll
+        for (int j = 0; j < MS; ++j, o += step)
+            if (mw + 16 * j < p.M)
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    const f32x4 v = value(i, j);
+                    const uint2 w = half ? make_uint2(F16::pack(v[0], v[1]), F16::pack(v[2], v[3]))
+                                         : make_uint2(Bf16::pack(v[0], v[1]), Bf16::pack(v[2], v[3]));
+                    if (whole) ((Loose8 *)(o + 16 * i))->v = w;
+                    else
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (nl + 16 * i + e < p.N) o[16 * i + e] = (uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
+                }
     }
 }
 
@@ -449,7 +577,7 @@ __global__ __launch_bounds__(64 * SKW) void gemm_few_kernel(GemmArgs p)
 #pragma unroll
         for (int w = 1; w < SKW; ++w) v += red[w][j][lane];
         const int m = 16 * j + r16;
-        if (m < p.M && nl < p.N) emit4(p, m, nl, v);
+        if (m < p.M && nl < p.N) emit4(p, blockIdx.y, m, nl, v);
     }
 }
 
@@ -506,9 +634,21 @@ GemmPlan plan_of(const cbr_gemm_shape &s)
     // Share k out until there is a workgroup for every CU, while each keeps min_kb blocks.
     int64_t splits = 1;
     if (tiles < 256) splits = std::max<int64_t>(1, std::min(256 / tiles, kbs / min_kb));
+    if (splits > 8) splits = splits / 8 * 8;
     p.kb_per = (int)up(kbs, splits);
     p.splits = (int)up(kbs, p.kb_per);
     return p;
+}
+
+template <int MS, int NS, int WM, int WN, int NST, int FA, int FB, int BB, bool WIDE>
+hipError_t launch_tile(const GemmPlan &pl, const GemmArgs &a, hipStream_t st)
+{
+    auto k = gemm_tile_kernel<MS, NS, WM, WN, NST, FA, FB, BB, WIDE>;
+    constexpr int lds = NST * stage_bytes<16 * MS * WM, 16 * NS * WN>();
+    static_assert(lds <= 160 * 1024, "LDS of a CU");
+    const hipError_t e = raise_lds_limit((const void *)k, lds);
+    if (e != hipSuccess) return e;
+    return launch(k, dim3((uint32_t)a.tiles_m * a.tiles_n * a.splits), dim3(64 * WM * WN), lds, st, nullptr, nullptr, a);
 }
 
 template <int FA, int FB, int BB>
@@ -519,14 +659,14 @@ hipError_t launch_formats(const GemmPlan &pl, const GemmArgs &a, hipStream_t st)
                  : pl.ms == 2 ? gemm_few_kernel<2, FA, FB, BB> : gemm_few_kernel<4, FA, FB, BB>;
         return launch(k, dim3(a.tiles_n, pl.splits), dim3(64 * SKW), 0, st, nullptr, nullptr, a);
     }
-    const bool big = pl.form == TILE256;
-    auto k = a.d_type == CBR_F32 ? gemm_tile_kernel<4, 4, 2, 2, FA, FB, BB, true>
-             : big ? gemm_tile_kernel<8, 4, 2, 4, FA, FB, BB, false> : gemm_tile_kernel<4, 4, 2, 2, FA, FB, BB, false>;
-    const int lds = 2 * (pl.bm + pl.bn) * BK;
-    const hipError_t e = raise_lds_limit((const void *)k, lds);
-    if (e != hipSuccess) return e;
-    return launch(k, dim3((uint32_t)(a.tiles_m * a.tiles_n), pl.splits), dim3(big ? 512 : 256), lds, st, nullptr, nullptr,
-                  a);
+    if (pl.form == TILE256) return launch_tile<8, 4, 2, 4, 2, FA, FB, BB, false>(pl, a, st);
+    // one workgroup a CU: four blocks deep; more: two, and two workgroups share a CU
+    const bool deep = (int64_t)a.tiles_m * a.tiles_n * pl.splits <= 256;
+    if (a.d_type == CBR_F32)
+        return deep ? launch_tile<4, 2, 2, 4, 4, FA, FB, BB, true>(pl, a, st)
+                    : launch_tile<4, 2, 2, 4, 2, FA, FB, BB, true>(pl, a, st);
+    return deep ? launch_tile<4, 2, 2, 4, 4, FA, FB, BB, false>(pl, a, st)
+                : launch_tile<4, 2, 2, 4, 2, FA, FB, BB, false>(pl, a, st);
 }
 
 }  // namespace
@@ -559,6 +699,7 @@ hipError_t launch_gemm_fp8(const cbr_gemm_shape &s, const void *a, const float *
     p.sb_ld = (int)((s.n + s.b_block - 1) / s.b_block);
     p.d_type = s.d_type;
     p.relu = s.relu;
+    p.splits = pl.splits;
     p.tiles_m = (int)((s.m + pl.bm - 1) / pl.bm);
     p.tiles_n = (int)((s.n + pl.bn - 1) / pl.bn);
     const bool a5 = s.a_type == CBR_E5M2, b5 = s.b_type == CBR_E5M2;

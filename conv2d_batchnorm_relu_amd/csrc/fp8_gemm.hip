@@ -247,6 +247,24 @@ __device__ __forceinline__ void place(const GemmArgs &p, int &tm, int &tn, int &
     tn = t / rows;
 }
 
+// Position of 16-byte chunk c of a row in LDS: c ^ perm.  The sixteen rows that a fragment read
+// covers (consecutive ones of a; of b as col_in_wave has them) then fall on all 64 banks.
+__device__ constexpr int perm(int row) { return (row >> 1) & 7; }
+template <bool WIDE>
+__device__ constexpr int perm_b(int row)
+{
+    return WIDE ? perm(row) : (((row >> 3) & 3) << 1) | ((row >> 1) & 1);
+}
+// Which of the wave's columns result e of lane group g in product i is.  16-bit outputs: the
+// two products of a pair make eight consecutive columns, one 16-byte store, and the four lane
+// groups of a row 64 bytes.  (Quads of 8 bytes, 32 bytes a row, made stores the bound:
+// 200704 x 128 x 512 took 92 us, 33 without its stores.)
+template <bool WIDE>
+__device__ constexpr int col_in_wave(int i, int g, int e)
+{
+    return WIDE ? 16 * i + 4 * g + e : 32 * (i >> 1) + 8 * g + 4 * (i & 1) + e;
+}
+
 // Tile kernel: 16 MS WM x 16 NS WN results a workgroup, WM x WN waves of 16 MS x 16 NS.
 // Both operands' rows of a k block (128 bytes) and their scales come straight into LDS, NST
 // blocks deep: while block t is multiplied, blocks t + 1 .. t + NST - 1 are on their way, and
@@ -266,6 +284,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
     static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN && NW >= 2, "tile shape");
     static_assert(64 * NW % BM == 0 && 64 * NW % BN == 0, "a scale's loads cover the tile evenly");
     static_assert(BB == 1 || 128 % (16 * NS) == 0, "a wave's columns lie in one block of b");
+    static_assert(NS % 2 == 0, "products in pairs");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const uint32_t lbase = (uint32_t)(uintptr_t)(lds_u8 *)lds;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -285,20 +304,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
     const __amdgpu_buffer_rsrc_t rb =
         __builtin_amdgcn_make_buffer_rsrc((void *)(p.b + (int64_t)n0 * p.ldb), 0, rows_b * p.ldb, 0x00020000);
     const int lrow = 8 * wave + (lane >> 3);
-    const int lchunk = 16 * ((lane & 7) ^ ((lrow >> 1) & 7));
+    const int lchunk = 16 * ((lane & 7) ^ perm(lrow)), lchunk_b = 16 * ((lane & 7) ^ perm_b<WIDE>(lrow));
     const int sa_at = wave * 64 % BM, sb_at = wave * 64 % BN;
     const int sb_n = BB == 1 ? rows_b : (rows_b + 127) / 128;
     auto load = [&](int kb, int st) __attribute__((always_inline)) {
-        const int kat = kb * BK + lchunk;
-        const bool in = kat < p.K;   // a chunk past K is not read: zeros
+        const int kat = kb * BK + lchunk, kbt = kb * BK + lchunk_b;   // a chunk past K is not read: zeros
         lds_u8 *base = (lds_u8 *)lds + st * STAGE;
         lds_u8 *dst = base + wave * 1024;
 #pragma unroll
         for (int t = 0; t < LA; ++t)
-            buffer_load_lds16(ra, dst + t * NW * 1024, in ? (lrow + t * 8 * NW) * p.lda + kat : (int)OOB);
+            buffer_load_lds16(ra, dst + t * NW * 1024, kat < p.K ? (lrow + t * 8 * NW) * p.lda + kat : (int)OOB);
 #pragma unroll
         for (int t = 0; t < LB; ++t)
-            buffer_load_lds16(rb, dst + BM * BK + t * NW * 1024, in ? (lrow + t * 8 * NW) * p.ldb + kat : (int)OOB);
+            buffer_load_lds16(rb, dst + BM * BK + t * NW * 1024, kbt < p.K ? (lrow + t * 8 * NW) * p.ldb + kbt : (int)OOB);
         // 64 scales a wave; where there are more waves than that, several load the same ones
         const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc(
             (void *)(p.sa + (int64_t)kb * p.M + m0), 0, rows_a * 4, 0x00020000);
@@ -314,11 +332,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
 #pragma unroll
         for (int j = 0; j < MS; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int frag = r16 * BK + 16 * (g ^ ((r16 >> 1) & 7));
-    const uint32_t fa0 = lbase + wm * 16 * MS * BK + frag;
-    const uint32_t fb0 = lbase + (BM + wn * 16 * NS) * BK + frag;
+    const uint32_t fa0 = lbase + (wm * 16 * MS + r16) * BK + 16 * (g ^ perm(r16));
+    const int brow = col_in_wave<WIDE>(0, r16 >> 2, r16 & 3);
+    const uint32_t fb0 = lbase + (BM + wn * 16 * NS + brow) * BK + 16 * (g ^ perm_b<WIDE>(brow));
     const uint32_t sa0 = lbase + SCALES + (wm * 16 * MS + r16) * 4;
-    const uint32_t sb0 = lbase + SCALES + BM * 4 + (BB == 1 ? wn * 16 * NS + 4 * g : wn * 16 * NS / 128) * 4;
+    const uint32_t sb0 = lbase + SCALES + BM * 4 + (BB == 1 ? wn * 16 * NS + col_in_wave<WIDE>(0, g, 0) : wn * 16 * NS / 128) * 4;
 
     const int turns = kb1 - kb0;
 #pragma unroll
@@ -338,7 +356,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
             // the chunk that K ends in: clear what lies past it
             const int kl = p.K - kb * BK, c = kl >> 4, cut = kl & 15;
             for (int r = threadIdx.x; r < BM + BN; r += 64 * NW) {
-                u32x4 *q = (u32x4 *)(lds + st * STAGE + r * BK + 16 * (c ^ ((r >> 1) & 7)));
+                u32x4 *q = (u32x4 *)(lds + st * STAGE + r * BK + 16 * (c ^ (r < BM ? perm(r) : perm_b<WIDE>(r - BM))));
                 u32x4 v = *q;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -360,15 +378,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         if constexpr (BB == 1)
             unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
                 constexpr int i = decltype(ic)::value;
-                t4[i] = __builtin_bit_cast(f32x4, lds_read16<i * 64>(sb0 + st * STAGE));
+                t4[i] = __builtin_bit_cast(f32x4, lds_read16<col_in_wave<WIDE>(i, 0, 0) * 4>(sb0 + st * STAGE));
             });
         else
             s1 = lds_read4<0>(sb0 + st * STAGE);
         u32x4 bf[NS][2], af[3][2];
         unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
             constexpr int i = decltype(ic)::value;
-            bf[i][0] = lds_read16<i * 16 * BK>(fb);
-            bf[i][1] = lds_read16<i * 16 * BK>(fbx);
+            bf[i][0] = lds_read16<col_in_wave<WIDE>(i, 0, 0) * BK>(fb);
+            bf[i][1] = lds_read16<col_in_wave<WIDE>(i, 0, 0) * BK>(fbx);
         });
         af[0][0] = lds_read16<0>(fa);
         af[0][1] = lds_read16<0>(fax);
@@ -442,8 +460,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         st = st + 1 == NST ? 0 : st + 1;
     }
     // Epilogue: bias (0 without one) and activation (a lower bound: 0, or none), then whole
-    // quads, or value by value in a tile that N ends in.
-    const int nl = n0 + wn * 16 * NS + 4 * g;
+    // chunks, or value by value in a tile that N ends in.
+    const int nl = n0 + wn * 16 * NS + col_in_wave<WIDE>(0, g, 0);
     const int64_t mw = m0 + wm * 16 * MS + r16;
     const bool whole = n0 + BN <= p.N, half = p.d_type == CBR_F16;
     const float *bias = p.part ? nullptr : p.bias;
@@ -451,13 +469,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
     f32x4 bv[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
+        const int n = nl + col_in_wave<WIDE>(i, 0, 0);
         bv[i] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (bias) {
-            if (whole) bv[i] = *(const f32x4 *)(bias + nl + 16 * i);
+            if (whole) bv[i] = *(const f32x4 *)(bias + n);
             else
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (nl + 16 * i + e < p.N) bv[i][e] = bias[nl + 16 * i + e];
+                    if (n + e < p.N) bv[i][e] = bias[n + e];
         }
     }
     auto value = [&](int i, int j) __attribute__((always_inline)) {
@@ -474,12 +493,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
             if (mw + 16 * j < p.M)
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
+                    const int c = col_in_wave<WIDE>(i, 0, 0);
                     const f32x4 v = value(i, j);
-                    if (whole) ((LooseF4 *)(o + 16 * i))->v = v;
+                    if (whole) ((LooseF4 *)(o + c))->v = v;
                     else
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (nl + 16 * i + e < p.N) o[16 * i + e] = v[e];
+                            if (nl + c + e < p.N) o[c + e] = v[e];
                 }
     } else {
         uint16_t *o = (uint16_t *)p.d + mw * p.N + nl;
@@ -487,15 +507,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         for (int j = 0; j < MS; ++j, o += step)
             if (mw + 16 * j < p.M)
 #pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    const f32x4 v = value(i, j);
-                    const uint2 w = half ? make_uint2(F16::pack(v[0], v[1]), F16::pack(v[2], v[3]))
-                                         : make_uint2(Bf16::pack(v[0], v[1]), Bf16::pack(v[2], v[3]));
-                    if (whole) ((Loose8 *)(o + 16 * i))->v = w;
+                for (int i = 0; i < NS; i += 2) {
+                    const int c = col_in_wave<WIDE>(i, 0, 0);
+                    const f32x4 v = value(i, j), w = value(i + 1, j);
+                    const u32x4 r = half ? u32x4{F16::pack(v[0], v[1]), F16::pack(v[2], v[3]), F16::pack(w[0], w[1]), F16::pack(w[2], w[3])}
+                                         : u32x4{Bf16::pack(v[0], v[1]), Bf16::pack(v[2], v[3]), Bf16::pack(w[0], w[1]), Bf16::pack(w[2], w[3])};
+                    if (whole) ((Loose16 *)(o + c))->v = r;
                     else
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (nl + 16 * i + e < p.N) o[16 * i + e] = (uint16_t)((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
+                        for (int e = 0; e < 8; ++e)
+                            if (nl + c + e < p.N) o[c + e] = (uint16_t)(r[e / 2] >> (16 * (e & 1)));
                 }
     }
 }
@@ -526,48 +547,75 @@ __global__ __launch_bounds__(64 * SKW) void gemm_few_kernel(GemmArgs p)
     f32x4 acc[MS];
 #pragma unroll
     for (int j = 0; j < MS; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto block = [&](int kb, auto &&get) __attribute__((always_inline)) {
-        Wide<FB> wb;
-        u32x4 lo, hi;
-        get(brow + kb * BK, lo, hi);
-        wb.set(lo, hi);
+    // One block's operands and scales, as loaded
+    struct Block {
+        u32x4 b[2], a[MS][2];
         f32x4 sb;
-        if constexpr (BB == 1) sb = scale4(p, kb, nl);
-        else sb[0] = p.sb[(int64_t)kb * p.sb_ld + n0 / 128];
+        float sa[MS];
+    };
+    auto fetch = [&](int kb, Block &o) __attribute__((always_inline)) {
+        o.b[0] = *(const u32x4 *)(brow + (int64_t)kb * BK);
+        o.b[1] = *(const u32x4 *)(brow + (int64_t)kb * BK + 16);
+#pragma unroll
+        for (int j = 0; j < MS; ++j) {
+            o.a[j][0] = *(const u32x4 *)(arow[j] + (int64_t)kb * BK);
+            o.a[j][1] = *(const u32x4 *)(arow[j] + (int64_t)kb * BK + 16);
+            o.sa[j] = p.sa[(int64_t)kb * p.M + mrow[j]];
+        }
+        if constexpr (BB == 1) o.sb = scale4(p, kb, nl);
+        else o.sb[0] = p.sb[(int64_t)kb * p.sb_ld + n0 / 128];
+    };
+    auto multiply = [&](const Block &o) __attribute__((always_inline)) {
+        Wide<FB> wb;
+        wb.set(o.b[0], o.b[1]);
 #pragma unroll
         for (int j = 0; j < MS; ++j) {
             Wide<FA> wa;
-            get(arow[j] + kb * BK, lo, hi);
-            wa.set(lo, hi);
+            wa.set(o.a[j][0], o.a[j][1]);
             f32x4 q = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int t = 0; t < 4; ++t) q = product(wb.t[t], wa.t[t], q);
-            const float s = p.sa[(int64_t)kb * p.M + mrow[j]];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(q[e] * sb[BB == 1 ? e : 0], s, acc[j][e]);
+            for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(q[e] * o.sb[BB == 1 ? e : 0], o.sa[j], acc[j][e]);
         }
     };
-    auto whole = [](const uint8_t *q, u32x4 &lo, u32x4 &hi) __attribute__((always_inline)) {
-        lo = *(const u32x4 *)q;
-        hi = *(const u32x4 *)(q + 16);
-    };
     const int full = min(kb1, p.K / BK);   // blocks that K does not end in
-    for (int kb = kb0 + wave; kb < full; kb += SKW) block(kb, whole);
+    int kb = kb0 + wave;
+    if (kb < full) {
+        Block now, next;
+        fetch(kb, now);
+        for (; kb + SKW < full; kb += SKW) {   // the next block loads while this one is multiplied
+            fetch(kb + SKW, next);
+            multiply(now);
+            now = next;
+        }
+        multiply(now);
+    }
     const int last = p.K / BK;
-    if (last >= kb0 && last < kb1 && (last - kb0) % SKW == wave && p.K % BK) {
+    if (p.K % BK && last >= kb0 && last < kb1 && (last - kb0) % SKW == wave) {
+        // the block that K ends in: only 16-byte chunks that begin before K are read, and what
+        // lies past K in the last of them is cleared
         const int left = p.K - last * BK - 32 * g;   // bytes of this lane's 32
-        block(last, [&](const uint8_t *q, u32x4 &lo, u32x4 &hi) __attribute__((always_inline)) {
-            lo = left > 0 ? *(const u32x4 *)q : u32x4{0u, 0u, 0u, 0u};
-            hi = left > 16 ? *(const u32x4 *)(q + 16) : u32x4{0u, 0u, 0u, 0u};
+        auto part = [&](const uint8_t *q, u32x4(&o)[2]) __attribute__((always_inline)) {
+            q += (int64_t)last * BK;
+            o[0] = left > 0 ? *(const u32x4 *)q : u32x4{0u, 0u, 0u, 0u};
+            o[1] = left > 16 ? *(const u32x4 *)(q + 16) : u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int keep = left - 4 * e;
-                const uint32_t w = e < 4 ? lo[e % 4] : hi[e % 4];
-                const uint32_t c = keep >= 4 ? w : keep <= 0 ? 0u : w & ((1u << (8 * keep)) - 1u);
-                if (e < 4) lo[e % 4] = c;
-                else hi[e % 4] = c;
+                if (keep < 4) o[e / 4][e % 4] = keep <= 0 ? 0u : o[e / 4][e % 4] & ((1u << (8 * keep)) - 1u);
             }
-        });
+        };
+        Block o;
+        part(brow, o.b);
+#pragma unroll
+        for (int j = 0; j < MS; ++j) {
+            part(arow[j], o.a[j]);
+            o.sa[j] = p.sa[(int64_t)last * p.M + mrow[j]];
+        }
+        if constexpr (BB == 1) o.sb = scale4(p, last, nl);
+        else o.sb[0] = p.sb[(int64_t)last * p.sb_ld + n0 / 128];
+        multiply(o);
     }
 #pragma unroll
     for (int j = 0; j < MS; ++j) red[wave][j][lane] = acc[j];
@@ -593,7 +641,15 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs p, int splits)
     const float *o = p.part + m * p.N + n;
     const int64_t step = p.M * p.N;
     if (n + 4 <= p.N) {
-        for (int s = 0; s < splits; ++s) v += ((const LooseF4 *)(o + s * step))->v;
+        int s = 0;
+        for (; s + 8 <= splits; s += 8) {   // eight loads under way, added in order
+            f32x4 w[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) w[u] = ((const LooseF4 *)(o + (s + u) * step))->v;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v += w[u];
+        }
+        for (; s < splits; ++s) v += ((const LooseF4 *)(o + s * step))->v;
     } else {
         for (int s = 0; s < splits; ++s)
             for (int e = 0; e < 3; ++e)
@@ -612,32 +668,57 @@ struct GemmPlan {
     int splits, kb_per;
 };
 
+// The tile and the number of splits with the least expected time, in us.  Measured on one
+// MI355X: a block of k takes `one` with one workgroup on a CU (256 at a time) and `two` with
+// two (512 at a time, 128-tiles), a workgroup's start and end `ends`; joining splits takes
+// 3 us and moves each part at 4 TB/s.  The 256-tile does twice the arithmetic for each byte
+// that a wave reads from LDS (8192^3: 484 us against 590), the 128-tile divides better (12544 x
+// 512 x 2048: 23 us against 38).
+struct Costs {
+    double one, two, ends;
+};
+
 GemmPlan plan_of(const cbr_gemm_shape &s)
 {
     const int64_t kbs = (s.k + BK - 1) / BK;
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    GemmPlan p{};
-    int64_t tiles, min_kb;
+    GemmPlan best{};
     if (s.m <= 64) {
-        p.form = FEW;
-        p.ms = s.m <= 16 ? 1 : s.m <= 32 ? 2 : 4;
-        p.bm = 16 * p.ms;
-        p.bn = 16;
-        min_kb = 2 * SKW;
-    } else {
-        const bool big = s.d_type != CBR_F32 && up(s.m, 256) * up(s.n, 256) >= 256;
-        p.form = big ? TILE256 : TILE128;
-        p.bm = p.bn = big ? 256 : 128;
-        min_kb = 8;
+        best.form = FEW;
+        best.ms = s.m <= 16 ? 1 : s.m <= 32 ? 2 : 4;
+        best.bm = 16 * best.ms;
+        best.bn = 16;
+        // k shared out among workgroups until every CU has one, two blocks a wave at least
+        const int64_t tiles = up(s.n, 16);
+        const int64_t splits = tiles < 256 ? std::max<int64_t>(1, std::min(256 / tiles, kbs / (2 * SKW))) : 1;
+        best.kb_per = (int)up(kbs, splits);
+        best.splits = (int)up(kbs, best.kb_per);
+        return best;
     }
-    tiles = up(s.m, p.bm) * up(s.n, p.bn);
-    // Share k out until there is a workgroup for every CU, while each keeps min_kb blocks.
-    int64_t splits = 1;
-    if (tiles < 256) splits = std::max<int64_t>(1, std::min(256 / tiles, kbs / min_kb));
-    if (splits > 8) splits = splits / 8 * 8;
-    p.kb_per = (int)up(kbs, splits);
-    p.splits = (int)up(kbs, p.kb_per);
-    return p;
+    const bool rows = s.b_block == 1;
+    double least = 0;
+    for (const Form form : {TILE128, TILE256}) {
+        if (form == TILE256 && s.d_type == CBR_F32) continue;
+        const Costs c = form == TILE256 ? (rows ? Costs{2.2, 0., 5.} : Costs{1.95, 0., 5.})
+                        : s.d_type == CBR_F32 ? (rows ? Costs{1.4, 2.6, 3.} : Costs{1.2, 2.0, 3.})
+                                              : (rows ? Costs{1.1, 1.25, 3.} : Costs{1.04, 1.15, 3.});
+        const int64_t edge = form == TILE256 ? 256 : 128, tiles = up(s.m, edge) * up(s.n, edge);
+        const int64_t most = tiles < 256 ? std::min(256 / tiles, kbs) : 1;
+        for (int64_t want = 1; want <= most; want += want < 8 ? 1 : 8) {   // see place() for eights
+            const int64_t per = up(kbs, want), splits = up(kbs, per), wgs = tiles * splits;
+            const double t = wgs <= 256 || form == TILE256 ? up(wgs, 256) * (per * c.one + c.ends)
+                                                           : up(wgs, 512) * (per * c.two + c.ends);
+            const double join = splits > 1 ? 3. + (double)splits * s.m * s.n * 8. / 4e6 : 0.;
+            if (best.splits == 0 || t + join < least) {
+                least = t + join;
+                best.form = form;
+                best.bm = best.bn = (int)edge;
+                best.kb_per = (int)per;
+                best.splits = (int)splits;
+            }
+        }
+    }
+    return best;
 }
 
 template <int MS, int NS, int WM, int WN, int NST, int FA, int FB, int BB, bool WIDE>

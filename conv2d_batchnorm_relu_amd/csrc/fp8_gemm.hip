@@ -523,7 +523,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
 
 // Few rows of a (m <= 16 MS): bound by reading b once.  A workgroup takes 16 columns, its
 // eight waves share the blocks of k, and both operands come from memory straight into the
-// product's registers (a row's 128 bytes of a block are read by four lanes, 32 each); the
+// product's registers (a row's 128 bytes of a block by four lanes, 64 bytes at a time); the
 // waves' sums are added through LDS in wave order.
 constexpr int SKW = 8;
 
@@ -536,13 +536,13 @@ __global__ __launch_bounds__(64 * SKW) void gemm_few_kernel(GemmArgs p)
     const int n0 = blockIdx.x * 16, nl = n0 + 4 * g;
     const int kb0 = blockIdx.y * p.kb_per, kb1 = min(p.kbs, kb0 + p.kb_per);
     // rows past the end read the last one; their results are not stored
-    const uint8_t *brow = p.b + (int64_t)min(n0 + r16, p.N - 1) * p.ldb + 32 * g;
+    const uint8_t *brow = p.b + (int64_t)min(n0 + r16, p.N - 1) * p.ldb + 16 * g;
     const uint8_t *arow[MS];
     int mrow[MS];
 #pragma unroll
     for (int j = 0; j < MS; ++j) {
         mrow[j] = min(16 * j + r16, (int)p.M - 1);
-        arow[j] = p.a + (int64_t)mrow[j] * p.lda + 32 * g;
+        arow[j] = p.a + (int64_t)mrow[j] * p.lda + 16 * g;
     }
     f32x4 acc[MS];
 #pragma unroll
@@ -555,11 +555,11 @@ __global__ __launch_bounds__(64 * SKW) void gemm_few_kernel(GemmArgs p)
     };
     auto fetch = [&](int kb, Block &o) __attribute__((always_inline)) {
         o.b[0] = *(const u32x4 *)(brow + (int64_t)kb * BK);
-        o.b[1] = *(const u32x4 *)(brow + (int64_t)kb * BK + 16);
+        o.b[1] = *(const u32x4 *)(brow + (int64_t)kb * BK + 64);
 #pragma unroll
         for (int j = 0; j < MS; ++j) {
             o.a[j][0] = *(const u32x4 *)(arow[j] + (int64_t)kb * BK);
-            o.a[j][1] = *(const u32x4 *)(arow[j] + (int64_t)kb * BK + 16);
+            o.a[j][1] = *(const u32x4 *)(arow[j] + (int64_t)kb * BK + 64);
             o.sa[j] = p.sa[(int64_t)kb * p.M + mrow[j]];
         }
         if constexpr (BB == 1) o.sb = scale4(p, kb, nl);
@@ -595,15 +595,17 @@ __global__ __launch_bounds__(64 * SKW) void gemm_few_kernel(GemmArgs p)
     if (p.K % BK && last >= kb0 && last < kb1 && (last - kb0) % SKW == wave) {
         // the block that K ends in: only 16-byte chunks that begin before K are read, and what
         // lies past K in the last of them is cleared
-        const int left = p.K - last * BK - 32 * g;   // bytes of this lane's 32
+        const int left = p.K - last * BK - 16 * g;   // bytes from this lane's first chunk on
         auto part = [&](const uint8_t *q, u32x4(&o)[2]) __attribute__((always_inline)) {
             q += (int64_t)last * BK;
-            o[0] = left > 0 ? *(const u32x4 *)q : u32x4{0u, 0u, 0u, 0u};
-            o[1] = left > 16 ? *(const u32x4 *)(q + 16) : u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int keep = left - 4 * e;
-                if (keep < 4) o[e / 4][e % 4] = keep <= 0 ? 0u : o[e / 4][e % 4] & ((1u << (8 * keep)) - 1u);
+            for (int h = 0; h < 2; ++h) {
+                o[h] = left > 64 * h ? *(const u32x4 *)(q + 64 * h) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int keep = left - 64 * h - 4 * e;
+                    if (keep < 4) o[h][e] = keep <= 0 ? 0u : o[h][e] & ((1u << (8 * keep)) - 1u);
+                }
             }
         };
         Block o;
@@ -683,6 +685,7 @@ GemmPlan plan_of(const cbr_gemm_shape &s)
     const int64_t kbs = (s.k + BK - 1) / BK;
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     GemmPlan best{};
+    double least = 0;
     if (s.m <= 64) {
         best.form = FEW;
         best.ms = s.m <= 16 ? 1 : s.m <= 32 ? 2 : 4;
@@ -693,10 +696,11 @@ GemmPlan plan_of(const cbr_gemm_shape &s)
         const int64_t splits = tiles < 256 ? std::max<int64_t>(1, std::min(256 / tiles, kbs / (2 * SKW))) : 1;
         best.kb_per = (int)up(kbs, splits);
         best.splits = (int)up(kbs, best.kb_per);
-        return best;
+        // b at 6.1 TB/s and, with every 16 columns reading all of a, 3.2% of that for each row
+        // (8192 x 8192: 13.1 us for 1 row, 17.8 for 16, 24.7 for 32, 40.2 for 64; tiles take 23)
+        least = 2. + (double)s.n * s.k / 6.1e6 * (1. + 0.032 * s.m) + (best.splits > 1 ? 3. : 0.);
     }
     const bool rows = s.b_block == 1;
-    double least = 0;
     for (const Form form : {TILE128, TILE256}) {
         if (form == TILE256 && s.d_type == CBR_F32) continue;
         const Costs c = form == TILE256 ? (rows ? Costs{2.2, 0., 5.} : Costs{1.95, 0., 5.})

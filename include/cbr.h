@@ -323,10 +323,10 @@ int cbr_fp8_quantize(const cbr_quant_shape *shape, const void *src, void *q, flo
  * [ceil(k/128)][m] (block 1), b_scale [ceil(k/128)][ceil(n / b_block)], b_block 1 or 128.
  * d [m][n] dense, d_type CBR_BF16, CBR_F16 or CBR_F32; bias float [n] or NULL; act is
  * max(v, 0) where relu is non-zero (a NaN stays one), else v.  Blocks are scaled and added
- * in fp32.  Within a block the sums are fp32 too for d_type CBR_F32 and for m <= 64; for
- * 16-bit outputs of more rows the 8-bit matrix instruction sums each eight consecutive
- * products with 13 bits below the leading one of the largest (about 1.3e-5 of the result's
- * norm), and everything beyond the eight in fp32.
+ * in fp32.  Within a block the sums are fp32 too for d_type CBR_F32; for 16-bit outputs the
+ * 8-bit matrix instruction may sum each eight consecutive products with 13 bits below the
+ * leading one of the largest (about 1.3e-5 of the result's norm), and everything beyond the
+ * eight in fp32.
  *   forward:          a = activations [pixels][C], b = filter [K][C] with b_block 128
  *   data gradient:    a = dy [pixels][K],          b = filter transposed [C][K], b_block 128
  *   weight gradient:  a = dy transposed [K][pixels], b = activations transposed, b_block 1

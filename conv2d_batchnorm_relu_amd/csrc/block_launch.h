@@ -21,7 +21,7 @@ struct BlockNormArgs {
     const void *dy, *dh;
     void *dx, *df, *dgate;
     float *dpost_w, *dpost_b, *dres_scale, *dpre_w, *dpre_b;
-    float *part;               // [blocks][4][C] partial sums over rows
+    float *part;               // the workgroups' partial sums over rows
 };
 
 hipError_t launch_block_norm_fwd(const BlockNormArgs &a, int stream_type, int branch_type, hipStream_t st);

@@ -82,22 +82,49 @@ __device__ __forceinline__ void load_vec(const float *p, float none, int l, int 
 
 constexpr int MAX_WAVES = 16;
 
-// Sums over the L threads of each row, for all rows of the workgroup at once: lane shuffles
-// within a wave (both operands of an addition are the same at both lanes, so every lane
-// holds the same sum), then, for rows of several waves, the waves' sums through LDS in wave
-// order.  Two halves of `red` take turns: a wave that is past the barrier of one sum may
-// write the next, never the one that others still read.
+// v plus the value of the lane across, for the steps of a sum over 2, 4, 8, 16, 32, 64 lanes:
+// neighbours, pairs, then quads and eights through mirrored rows (their lanes hold one value
+// by then), 16-lane rows and halves by swapping them.  Register moves beside the vector unit:
+// a lane shuffle through LDS takes some ten times as long, six of them in a row per sum.
+template <int STEP>
+__device__ __forceinline__ float add_across(float v)
+{
+    constexpr int CTRL[4] = {0xB1, 0x4E, 0x141, 0x140};   // quad_perm 1032, 2301; row_half_mirror, row_mirror
+    const int b = __float_as_int(v);
+    if constexpr (STEP < 4) {
+        return v + __int_as_float(__builtin_amdgcn_mov_dpp(b, CTRL[STEP], 0xf, 0xf, true));
+    } else {
+        // both results hold a row (half) and the one across in the same order at every lane
+        const auto r = STEP == 4 ? __builtin_amdgcn_permlane16_swap(b, b, false, false)
+                                 : __builtin_amdgcn_permlane32_swap(b, b, false, false);
+        return __int_as_float(r[0]) + __int_as_float(r[1]);
+    }
+}
+
+// Sums over the L threads of each row, for all rows of the workgroup at once: within a wave
+// (both operands of an addition are the same at both lanes, so every lane holds the same sum),
+// then, for rows of several waves, the waves' sums through LDS in wave order.  Two halves of
+// `red` take turns: a wave that is past the barrier of one sum may write the next, never the
+// one that others still read.
 template <int NV>
 struct RowSum {
     float (*red)[MAX_WAVES][NV];   // [2][MAX_WAVES][NV]
     int L, turn;
 
+    template <int STEP>
+    __device__ __forceinline__ void step(float (&v)[NV])
+    {
+        if constexpr (STEP < 6) {
+            if (L <= 1 << STEP) return;
+#pragma unroll
+            for (int e = 0; e < NV; ++e) v[e] = add_across<STEP>(v[e]);
+            step<STEP + 1>(v);
+        }
+    }
+
     __device__ __forceinline__ void operator()(float (&v)[NV])
     {
-        const int w = L < 64 ? L : 64;
-        for (int off = 1; off < w; off <<= 1)
-#pragma unroll
-            for (int e = 0; e < NV; ++e) v[e] += __shfl_xor(v[e], off);
+        step<0>(v);
         if (L > 64) {
             const int wave = threadIdx.x >> 6, per = L >> 6, first = wave / per * per;
             if ((threadIdx.x & 63) == 0)

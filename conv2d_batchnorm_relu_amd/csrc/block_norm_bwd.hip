@@ -16,31 +16,42 @@ namespace {
 
 using namespace bnorm;
 
-// How the rows are dealt out.  SPLIT: a gate row's rows go to `per` workgroups, each within
-// one gate row, and the partial sums are S1, S0, T1, T0 of that gate row.  Otherwise every
-// group of L threads owns `gates` whole gate rows: it finishes their dgate itself and the
-// partial sums are sum g S1, sum g S0, T1, T0.
+// How the rows are dealt out (Deal below).  split: a gate row's rows go to `per` workgroups,
+// each within one gate row, and the partial sums are S1, S0, T1, T0 of that gate row.
+// Otherwise every group of L threads owns `gates` whole gate rows: it finishes their dgate
+// itself and the partial sums are sum g S1, sum g S0, T1, T0.
+
+// Floats from a partial row (four quantities of C channels) to the next.  The 64 beyond them
+// put the rows of a channel on different memory channels: with a stride of 4 KB (C = 256) the
+// kernel that adds 512 of them took 19 us.
+__host__ __device__ constexpr size_t part_ld(int C) { return 4 * (size_t)C + 64; }
+
+constexpr int BWD_THREADS = 512;
+// Workgroups that run at once: one of 512 threads a CU (155 to 230 registers a thread).  With
+// two or three times as many, or with two on a CU at 128 registers, the partial rows and the
+// spilled registers cost more than the waves hide (4096 x 4096: 78 us; 512 workgroups 91, at
+// 128 registers 114, 768 of 256 threads 99).
+constexpr int BWD_BLOCKS = 256;
+
 struct Deal {
+    Layout o;
     int blocks, per, gates;
     bool split;
 };
 
-constexpr int BWD_THREADS = 512;
-// Workgroups at most: two of 512 threads fit a CU's registers at a time (a partial row is 16
-// bytes a channel written and read again, so more workgroups than run at once only add bytes).
-constexpr int BWD_BLOCKS = 512;
-
-Deal deal_of(uint32_t rows, uint32_t rpg, bool gate, const Layout &o)
+Deal deal_of(uint32_t rows, uint32_t rpg, bool gate, int C)
 {
     const uint64_t gates = gate ? rows / rpg : 1;
     if (!gate) rpg = rows;
     auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
-    const uint64_t subs = (uint64_t)BWD_BLOCKS * o.rpb;
-    // rows in turn of the busiest group of threads, either way
-    const uint64_t per = std::max<uint64_t>(1, std::min<uint64_t>(BWD_BLOCKS / gates, rpg / (2u * o.rpb)));
-    const uint64_t split_turns = up(gates * per, BWD_BLOCKS) * up(up(rpg, per), o.rpb);
-    const uint64_t whole_turns = up(gates, subs) * rpg;
     Deal d;
+    d.o = layout_of(C, BWD_THREADS, BWD_THREADS);
+    const uint64_t subs = (uint64_t)BWD_BLOCKS * d.o.rpb;
+    // Rows in turn of the busiest group of threads either way; a workgroup's start and end (its
+    // coefficients, its partial row) cost about eight.
+    const uint64_t per = std::max<uint64_t>(1, std::min<uint64_t>(BWD_BLOCKS / gates, rpg / d.o.rpb));
+    const uint64_t split_turns = up(gates * per, BWD_BLOCKS) * (up(up(rpg, per), d.o.rpb) + 8);
+    const uint64_t whole_turns = up(gates, subs) * rpg + 8;
     d.split = !gate || split_turns < whole_turns;
     if (d.split) {
         d.per = (int)per;
@@ -49,7 +60,10 @@ Deal deal_of(uint32_t rows, uint32_t rpg, bool gate, const Layout &o)
     } else {
         d.per = 1;
         d.gates = (int)up(gates, subs);
-        d.blocks = (int)up(up(gates, d.gates), o.rpb);
+        const uint64_t groups = up(gates, d.gates);
+        // few groups: in smaller workgroups, to reach every CU
+        if (groups < subs / 2) d.o = layout_of(C, BWD_THREADS / 2, BWD_THREADS);
+        d.blocks = (int)up(groups, d.o.rpb);
     }
     return d;
 }
@@ -82,12 +96,15 @@ __global__ __launch_bounds__(BWD_THREADS) void block_norm_bwd_kernel(BlockNormAr
         turns = (uint32_t)own;
     }
 
-    float ar[E], w[E], pw[E];        // alpha r (SPLIT: alpha r g), post_w, pre_w
-    load_vec<E, TAIL>(p.res_scale, 1.f, l, L, C, ar);
-    load_vec<E, TAIL>(p.post_w, 1.f, l, L, C, w);
-    load_vec<E, TAIL>(p.pre_w, 1.f, l, L, C, pw);
+    float cw[E], pw[E];        // alpha r post_w (SPLIT: times g), pre_w
+    {
+        float w[E];
+        load_vec<E, TAIL>(p.res_scale, 1.f, l, L, C, cw);
+        load_vec<E, TAIL>(p.post_w, 1.f, l, L, C, w);
+        load_vec<E, TAIL>(p.pre_w, 1.f, l, L, C, pw);
 #pragma unroll
-    for (int j = 0; j < E; ++j) ar[j] *= p.alpha;
+        for (int j = 0; j < E; ++j) cw[j] *= p.alpha * w[j];
+    }
     Row<TB, E, TAIL> graw;
     if constexpr (SPLIT) {
         if (p.gate) {
@@ -95,7 +112,7 @@ __global__ __launch_bounds__(BWD_THREADS) void block_norm_bwd_kernel(BlockNormAr
             graw.load((const char *)p.gate + (uint64_t)(blockIdx.x / per) * C * TB::SIZE, l, L, C, true);
             graw.get(gv);
 #pragma unroll
-            for (int j = 0; j < E; ++j) ar[j] *= gv[j];
+            for (int j = 0; j < E; ++j) cw[j] *= gv[j];
         }
     }
     float s1[E], s0[E], t1[E], t0[E], g1[SPLIT ? 1 : E], g0[SPLIT ? 1 : E];
@@ -170,10 +187,9 @@ __global__ __launch_bounds__(BWD_THREADS) void block_norm_bwd_kernel(BlockNormAr
                 if (haspost) f[j] = in ? (f[j] - qs.x) * qs.y : 0.f;   // nhat
                 s1[j] = fmaf(d[j], f[j], s1[j]);
                 s0[j] += d[j];
-                d[j] *= ar[j];
+                d[j] *= cw[j];
                 if constexpr (!SPLIT) d[j] *= g[j];
                 if (haspost) {
-                    d[j] *= w[j];
                     m[0] = fmaf(d[j], f[j], m[0]);
                     m[1] += d[j];
                 }
@@ -189,10 +205,12 @@ __global__ __launch_bounds__(BWD_THREADS) void block_norm_bwd_kernel(BlockNormAr
                 if (--left == 0) {   // the gate row is done
                     left = p.rpg;
                     if (on && p.dgate) {
-                        float pb[E], o[E];
+                        float w[E], r[E], pb[E], o[E];
+                        load_vec<E, TAIL>(p.post_w, 1.f, l, L, C, w);
                         load_vec<E, TAIL>(p.post_b, 0.f, l, L, C, pb);
+                        load_vec<E, TAIL>(p.res_scale, 1.f, l, L, C, r);
 #pragma unroll
-                        for (int j = 0; j < E; ++j) o[j] = ar[j] * fmaf(w[j], s1[j], pb[j] * s0[j]);
+                        for (int j = 0; j < E; ++j) o[j] = p.alpha * r[j] * fmaf(w[j], s1[j], pb[j] * s0[j]);
                         Row<TB, E, TAIL>::store((char *)p.dgate + (uint64_t)((uint32_t)row / p.rpg) * C * TB::SIZE, l,
                                                L, C, o);
                     }
@@ -222,31 +240,54 @@ __global__ __launch_bounds__(BWD_THREADS) void block_norm_bwd_kernel(BlockNormAr
         __syncthreads();
         for (int c = threadIdx.x; c < C; c += blockDim.x) {
             float v = comb[c];
-            for (int s = 1; s < rpb; ++s) v += comb[s * L * E + c];
-            p.part[((size_t)blockIdx.x * 4 + q) * C + c] = v;
+            int s = 1;
+            for (; s + 4 <= rpb; s += 4) {   // four reads under way, added in order
+                const float a = comb[s * L * E + c], b = comb[(s + 1) * L * E + c];
+                const float d = comb[(s + 2) * L * E + c], f = comb[(s + 3) * L * E + c];
+                v = v + a + b + d + f;
+            }
+            for (; s < rpb; ++s) v += comb[s * L * E + c];
+            p.part[blockIdx.x * part_ld(C) + (size_t)q * C + c] = v;
         }
     }
 }
 
 // The parameters' gradients from the partial rows, in fp64 and a fixed order.  Blocks
-// 0 .. nparam - 1 take 16 channels each: 64 threads a channel over the partial rows, added
-// through LDS.  The blocks after them (dgate of a split gate row): 256 channels of one gate
-// row each, a thread a channel.
-constexpr int FIN_CH = 16, FIN_RG = 64, FIN_THREADS = FIN_CH * FIN_RG;
+// 0 .. nparam - 1 take 64 channels of one norm's pair of sums each: sixteen waves share the
+// partial rows (a wave reads 256 bytes of a row, FIN_UN rows' loads under way together) and
+// are added through LDS in wave order.  (Lane shuffles of fp64 values cost more than the
+// loads: 6.6 us against 4 on the smallest case.)  The blocks after them (dgate of a split
+// gate row): 1024 channels of one gate row each, a thread a channel.
+constexpr int FIN_RG = 16, FIN_THREADS = 64 * FIN_RG, FIN_UN = 8;
 
 template <typename TB>
 __global__ __launch_bounds__(FIN_THREADS) void block_norm_bwd_finish_kernel(BlockNormArgs p, int blocks, int per,
                                                                             int split, int nparam)
 {
-    __shared__ double red[4][FIN_RG][FIN_CH];
+    __shared__ double red[2][FIN_RG][64];
     const int C = p.C;
     if ((int)blockIdx.x >= nparam) {
-        const int tiles = (C + 255) / 256, b = blockIdx.x - nparam;
-        const int gi = b / tiles, c = b % tiles * 256 + threadIdx.x;
-        if (threadIdx.x >= 256 || c >= C) return;
+        const int tiles = (C + FIN_THREADS - 1) / FIN_THREADS, b = blockIdx.x - nparam;
+        const int gi = b / tiles, c = b % tiles * FIN_THREADS + threadIdx.x;
+        if (c >= C) return;
+        const size_t ld = part_ld(C);
+        const float *row = p.part + (size_t)gi * per * ld + c;
         double s1 = 0., s0 = 0.;
-        for (int k = 0; k < per; ++k) {
-            const float *row = p.part + ((size_t)gi * per + k) * 4 * C + c;
+        int k = 0;
+        for (; k + 4 <= per; k += 4, row += 4 * ld) {
+            float a[4], z[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                a[u] = row[u * ld];
+                z[u] = row[u * ld + C];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                s1 += a[u];
+                s0 += z[u];
+            }
+        }
+        for (; k < per; ++k, row += ld) {
             s1 += row[0];
             s0 += row[C];
         }
@@ -255,41 +296,51 @@ __global__ __launch_bounds__(FIN_THREADS) void block_norm_bwd_finish_kernel(Bloc
         store_one<TB>((char *)p.dgate + ((size_t)gi * C + c) * TB::SIZE, (float)(ar * (w * s1 + pb * s0)));
         return;
     }
-    const int ch = threadIdx.x % FIN_CH, rg = threadIdx.x / FIN_CH;
-    const int c = blockIdx.x * FIN_CH + ch;
-    double v[4] = {0., 0., 0., 0.};
-    if (c < C)
-        for (int b = rg; b < blocks; b += FIN_RG) {
-            const float *row = p.part + (size_t)b * 4 * C + c;
-            double g = 1.0;
-            if (split && p.gate)
-                g = to_float<TB>(load_bits<TB>((const char *)p.gate + ((size_t)(b / per) * C + c) * TB::SIZE));
-            if (p.f) {
-                v[0] += g * row[0];
-                v[1] += g * row[C];
+    const bool hasf = p.f != nullptr, haspre = p.pre != CBR_NORM_NONE;
+    // which pair: the post norm's S1, S0 or the pre norm's T1, T0 (those that exist)
+    const bool post = hasf && (!haspre || blockIdx.x % 2 == 0);
+    const int c = (hasf && haspre ? blockIdx.x / 2 : blockIdx.x) * 64 + threadIdx.x % 64, rg = threadIdx.x / 64;
+    const bool weigh = post && split && p.gate;
+    double s1 = 0., s0 = 0.;
+    if (c < C) {
+        const float *rows = p.part + (post ? 0 : 2 * (size_t)C) + c;
+        for (int b0 = rg; b0 < blocks; b0 += FIN_RG * FIN_UN) {
+            float a[FIN_UN], z[FIN_UN];
+            uint32_t g[FIN_UN];   // as loaded: converted here, each would be waited for
+#pragma unroll
+            for (int u = 0; u < FIN_UN; ++u) {
+                const int b = min(b0 + u * FIN_RG, blocks - 1);   // past the end: read, not added
+                a[u] = rows[b * part_ld(C)];
+                z[u] = rows[b * part_ld(C) + C];
+                if (weigh) g[u] = load_bits<TB>((const char *)p.gate + ((size_t)(b / per) * C + c) * TB::SIZE);
             }
-            if (p.pre != CBR_NORM_NONE) {
-                v[2] += row[2 * (size_t)C];
-                v[3] += row[3 * (size_t)C];
-            }
+#pragma unroll
+            for (int u = 0; u < FIN_UN; ++u)
+                if (b0 + u * FIN_RG < blocks) {
+                    const float gv = weigh ? to_float<TB>(g[u]) : 1.f;
+                    s1 += (double)gv * a[u];
+                    s0 += (double)gv * z[u];
+                }
         }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) red[q][rg][ch] = v[q];
-    for (int half = FIN_RG / 2; half > 0; half /= 2) {
-        __syncthreads();
-        if (rg < half)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) red[q][rg][ch] += red[q][rg + half][ch];
     }
+    red[0][rg][threadIdx.x % 64] = s1;
+    red[1][rg][threadIdx.x % 64] = s0;
+    __syncthreads();
     if (rg != 0 || c >= C) return;
-    const double s1 = red[0][0][ch], s0 = red[1][0][ch];
-    const double w = p.post_w ? p.post_w[c] : 1.0, pb = p.post_b ? p.post_b[c] : 0.0;
-    const double r = p.res_scale ? p.res_scale[c] : 1.0, al = p.alpha;
-    if (p.dres_scale) p.dres_scale[c] = (float)(al * (w * s1 + pb * s0));
-    if (p.dpost_w) p.dpost_w[c] = (float)(al * r * s1);
-    if (p.dpost_b) p.dpost_b[c] = (float)(al * r * s0);
-    if (p.dpre_w) p.dpre_w[c] = (float)red[2][0][ch];
-    if (p.dpre_b) p.dpre_b[c] = (float)red[3][0][ch];
+    for (int i = 1; i < FIN_RG; ++i) {
+        s1 += red[0][i][threadIdx.x];
+        s0 += red[1][i][threadIdx.x];
+    }
+    if (post) {
+        const double w = p.post_w ? p.post_w[c] : 1.0, pb = p.post_b ? p.post_b[c] : 0.0;
+        const double r = p.res_scale ? p.res_scale[c] : 1.0, al = p.alpha;
+        if (p.dres_scale) p.dres_scale[c] = (float)(al * (w * s1 + pb * s0));
+        if (p.dpost_w) p.dpost_w[c] = (float)(al * r * s1);
+        if (p.dpost_b) p.dpost_b[c] = (float)(al * r * s0);
+    } else {
+        if (p.dpre_w) p.dpre_w[c] = (float)s1;
+        if (p.dpre_b) p.dpre_b[c] = (float)s0;
+    }
 }
 
 using Kernel = void (*)(BlockNormArgs, int, int, int, int);
@@ -304,8 +355,8 @@ Kernel kernel_of(bool tail, bool split)
 template <typename TS, typename TB>
 hipError_t launch_types(BlockNormArgs a, hipStream_t st)
 {
-    const Layout o = layout_of(a.C, BWD_THREADS, BWD_THREADS);
-    const Deal d = deal_of(a.rows, a.rpg, a.gate != nullptr, o);
+    const Deal d = deal_of(a.rows, a.rpg, a.gate != nullptr, a.C);
+    const Layout &o = d.o;
     if (!a.gate) a.rpg = a.rows;
     const bool params = a.dres_scale || a.dpost_w || a.dpost_b || a.dpre_w || a.dpre_b;
     const bool gates = a.dgate && d.split;
@@ -313,8 +364,9 @@ hipError_t launch_types(BlockNormArgs a, hipStream_t st)
     auto k = o.E == 8 ? kernel_of<TS, TB, 8>(o.tail, d.split) : kernel_of<TS, TB, 16>(o.tail, d.split);
     hipError_t e = launch(k, dim3(d.blocks), dim3(o.threads), 0, st, nullptr, nullptr, a, o.L, o.rpb, d.per, d.gates);
     if (e != hipSuccess || !a.part) return e;
-    const int nparam = params ? (a.C + FIN_CH - 1) / FIN_CH : 0;
-    const int ngate = gates ? d.blocks / d.per * ((a.C + 255) / 256) : 0;
+    const int pairs = (a.f != nullptr) + (a.pre != CBR_NORM_NONE);
+    const int nparam = params ? pairs * ((a.C + 63) / 64) : 0;
+    const int ngate = gates ? d.blocks / d.per * ((a.C + FIN_THREADS - 1) / FIN_THREADS) : 0;
     return launch(block_norm_bwd_finish_kernel<TB>, dim3(nparam + ngate), dim3(FIN_THREADS), 0, st, nullptr, nullptr, a,
                   d.blocks, d.per, (int)d.split, nparam);
 }
@@ -323,10 +375,9 @@ hipError_t launch_types(BlockNormArgs a, hipStream_t st)
 
 size_t block_norm_part_bytes(uint32_t rows, uint32_t rpg, int C)
 {
-    const Layout o = layout_of(C, BWD_THREADS, BWD_THREADS);
-    int blocks = deal_of(rows, rows, false, o).blocks;
-    if (rpg) blocks = std::max(blocks, deal_of(rows, rpg, true, o).blocks);
-    return (size_t)blocks * 4 * C * sizeof(float);
+    int blocks = deal_of(rows, rows, false, C).blocks;
+    if (rpg) blocks = std::max(blocks, deal_of(rows, rpg, true, C).blocks);
+    return blocks * part_ld(C) * sizeof(float);
 }
 
 hipError_t launch_block_norm_bwd(const BlockNormArgs &a, int stream_type, int branch_type, hipStream_t st)

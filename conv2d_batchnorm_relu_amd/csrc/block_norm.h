@@ -30,23 +30,37 @@ template <typename T, int E, bool TAIL>
 struct Row {
     Raw8<T> c[E / 8];
 
-    // row: byte address of the row's channel 0; on false nothing is read and the values are 0
+    // row: byte address of the row's channel 0; on false nothing is read and the values are 0.
+    // The last, partial chunk of a row is loaded as the row's last eight values and moved to the
+    // front when it is used (get): one access like the others, in flight beside the sums.  Value
+    // by value, the loads would be waited for here.
     __device__ __forceinline__ void load(const char *row, int l, int L, int C, bool on)
     {
 #pragma unroll
         for (int i = 0; i < E / 8; ++i) {
             const int col = 8 * (i * L + l);
-            const char *p = row + (size_t)col * T::SIZE;
-            if (on && col + (TAIL ? 8 : 1) <= C) load_raw8<T, TAIL>(p, c[i]);
-            else if (TAIL && on && col < C) load_part8<T>(p, C - col, c[i]);
-            else c[i] = Raw8<T>{};
+            if (TAIL && C < 8) {
+                if (on && col < C) load_part8<T>(row, C, c[i]);
+                else c[i] = Raw8<T>{};
+            } else if (on && col < C) {
+                load_raw8<T, TAIL>(row + (size_t)(TAIL ? min(col, C - 8) : col) * T::SIZE, c[i]);
+            } else {
+                c[i] = Raw8<T>{};
+            }
         }
     }
 
-    __device__ __forceinline__ void get(float (&o)[E]) const
+    __device__ __forceinline__ void get(float (&o)[E], int l, int L, int C) const
     {
 #pragma unroll
-        for (int i = 0; i < E / 8; ++i) unpack8<T>(c[i], o + 8 * i);
+        for (int i = 0; i < E / 8; ++i) {
+            Raw8<T> r = c[i];
+            if (TAIL && C >= 8) {
+                const int col = 8 * (i * L + l);
+                drop8<T>(r, 8 - (C & 7), col < C && col + 8 > C);
+            }
+            unpack8<T>(r, o + 8 * i);
+        }
     }
 
     static __device__ __forceinline__ void store(char *row, int l, int L, int C, const float (&v)[E])
@@ -73,7 +87,7 @@ __device__ __forceinline__ void load_vec(const float *p, float none, int l, int 
     if (p) {
         Row<F32, E, TAIL> r;
         r.load((const char *)p, l, L, C, true);
-        r.get(o);
+        r.get(o, l, L, C);
     } else {
 #pragma unroll
         for (int j = 0; j < E; ++j) o[j] = none;

@@ -110,7 +110,7 @@ __global__ __launch_bounds__(BWD_THREADS) void block_norm_bwd_kernel(BlockNormAr
         if (p.gate) {
             float gv[E];
             graw.load((const char *)p.gate + (uint64_t)(blockIdx.x / per) * C * TB::SIZE, l, L, C, true);
-            graw.get(gv);
+            graw.get(gv, l, L, C);
 #pragma unroll
             for (int j = 0; j < E; ++j) cw[j] *= gv[j];
         }
@@ -144,10 +144,10 @@ __global__ __launch_bounds__(BWD_THREADS) void block_norm_bwd_kernel(BlockNormAr
         const bool on = row < r1;
         if constexpr (!AHEAD) fetch(row);
         float d[E], a[E], b[E], f[E];
-        dyn.get(d);
-        yn.get(a);
-        dhn.get(b);
-        fn.get(f);
+        dyn.get(d, l, L, C);
+        yn.get(a, l, L, C);
+        dhn.get(b, l, L, C);
+        fn.get(f, l, L, C);
         const f32x2 ps = psn, qs = qsn;
         if constexpr (!SPLIT)
             if (p.gate && left == p.rpg)
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(BWD_THREADS) void block_norm_bwd_kernel(BlockNormAr
             float m[2] = {0.f, 0.f};
             float g[SPLIT ? 1 : E];
             if constexpr (!SPLIT) {
-                if (p.gate) graw.get(g);
+                if (p.gate) graw.get(g, l, L, C);
                 else
 #pragma unroll
                     for (int j = 0; j < E; ++j) g[j] = 1.f;

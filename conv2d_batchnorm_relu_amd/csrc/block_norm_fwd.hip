@@ -74,8 +74,8 @@ __global__ __launch_bounds__(1024) void block_norm_fwd_kernel(BlockNormArgs p, i
     fetch(row);
     for (uint32_t t = 0; t < turns; ++t, row += step) {
         float v[E], y[E];
-        xn.get(y);
-        fn.get(v);
+        xn.get(y, l, L, C);
+        fn.get(v, l, L, C);
         const bool on = row < p.rows;
         Row<TB, E, TAIL> g;
         if (p.gate)
@@ -89,7 +89,7 @@ __global__ __launch_bounds__(1024) void block_norm_fwd_kernel(BlockNormArgs p, i
             }
             if (p.gate) {
                 float gv[E];
-                g.get(gv);
+                g.get(gv, l, L, C);
 #pragma unroll
                 for (int j = 0; j < E; ++j) y[j] = fmaf(gv[j], fmaf(cw[j], v[j], cb[j]), y[j]);
             } else {
@@ -113,7 +113,9 @@ hipError_t launch_types(const BlockNormArgs &a, hipStream_t st)
 {
     const Layout o = layout_of(a.C, 256, 1024);
     const uint32_t need = (uint32_t)(((uint64_t)a.rows + o.rpb - 1) / o.rpb);
-    const uint32_t grid = std::min<uint32_t>(need, 256u * (2048u / o.threads));
+    // As many workgroups as run at once (sixteen waves a CU), each with the same number of rows
+    const uint32_t most = 256u * std::max(1u, 1024u / o.threads), turns = (need + most - 1) / most;
+    const uint32_t grid = (need + turns - 1) / turns;
     auto k = o.tail ? block_norm_fwd_kernel<TS, TB, true> : block_norm_fwd_kernel<TS, TB, false>;
     return launch(k, dim3(grid), dim3(o.threads), 0, st, nullptr, nullptr, a, o.L, o.rpb);
 }

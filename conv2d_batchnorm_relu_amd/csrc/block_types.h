@@ -123,6 +123,31 @@ __device__ __forceinline__ void load_part8(const char *p, int n, Raw8<T> &r)
         }
 }
 
+// Moves the last 8 - s of eight values (s = 0..7, the same in all lanes) to the front, zeros
+// behind them, in the lanes where `on`.
+template <typename T>
+__device__ __forceinline__ void drop8(Raw8<T> &r, int s, bool on)
+{
+    constexpr int W = T::WORDS;
+    uint32_t w[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = r.v[i / 4][i % 4];
+    auto words = [&](int by) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = on ? (i + by < W ? w[i + by] : 0u) : w[i];
+    };
+    if (s & 4) words(W / 2);
+    if (s & 2) words(W / 4);
+    if (s & 1) {
+        if constexpr (T::SIZE == 4) words(1);
+        else
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[i] = on ? w[i] >> 16 | (i + 1 < W ? w[i + 1] << 16 : 0u) : w[i];
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) r.v[i / 4][i % 4] = w[i];
+}
+
 template <typename T>
 __device__ __forceinline__ void store_part8(char *p, int n, const float *v)
 {

@@ -10,23 +10,26 @@ namespace bnorm {
 
 // A row is held by L threads, E values each (8 or 16): L a power of two up to 64 (then
 // several rows share a wave), or a multiple of 64 (several waves share a row).  Thread l's
-// values 8i..8i+7 are channels 8 (i L + l) .. + 7, one 16- or 32-byte access.  TAIL (C % 8
-// != 0): rows start at any value's address and the last chunk of a row is a part of one.
+// values 8i..8i+7 are channels 8 (i L + l) .. + 7, one 16- or 32-byte access.  Tail says what
+// the last chunk of a row is: a whole one (C % 8 == 0), a part of one in rows that start at
+// any value's address, or (C < 8) a part that is all of the row.
+enum Tail { WHOLE = 0, PART = 1, SHORT = 2 };
+
 template <int E>
 __device__ __forceinline__ int col_of(int j, int l, int L)
 {
     return 8 * ((j >> 3) * L + l) + (j & 7);
 }
 
-// Whether value j exists (!TAIL: the same answer for the eight values of a chunk).
-template <int E, bool TAIL>
+// Whether value j exists (WHOLE: the same answer for the eight values of a chunk).
+template <int E, Tail TAIL>
 __device__ __forceinline__ bool has(int j, int l, int L, int C)
 {
     return col_of<E>(TAIL ? j : (j & ~7), l, L) < C;
 }
 
 // A thread's values of one row of a tensor of type T, as they sit in memory.
-template <typename T, int E, bool TAIL>
+template <typename T, int E, Tail TAIL>
 struct Row {
     Raw8<T> c[E / 8];
 
@@ -39,14 +42,9 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < E / 8; ++i) {
             const int col = 8 * (i * L + l);
-            if (TAIL && C < 8) {
-                if (on && col < C) load_part8<T>(row, C, c[i]);
-                else c[i] = Raw8<T>{};
-            } else if (on && col < C) {
-                load_raw8<T, TAIL>(row + (size_t)(TAIL ? min(col, C - 8) : col) * T::SIZE, c[i]);
-            } else {
-                c[i] = Raw8<T>{};
-            }
+            if (!on || col >= C) c[i] = Raw8<T>{};
+            else if (TAIL == SHORT) load_part8<T>(row, C, c[i]);
+            else load_raw8<T, TAIL == PART>(row + (size_t)(TAIL == PART ? min(col, C - 8) : col) * T::SIZE, c[i]);
         }
     }
 
@@ -55,7 +53,7 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < E / 8; ++i) {
             Raw8<T> r = c[i];
-            if (TAIL && C >= 8) {
+            if (TAIL == PART) {
                 const int col = 8 * (i * L + l);
                 drop8<T>(r, 8 - (C & 7), col < C && col + 8 > C);
             }
@@ -72,7 +70,7 @@ struct Row {
             if (col + (TAIL ? 8 : 1) <= C) {
                 Raw8<T> r;
                 pack8<T>(v + 8 * i, r);
-                store_raw8<T, TAIL>(p, r);
+                store_raw8<T, TAIL != WHOLE>(p, r);
             } else if (TAIL && col < C) {
                 store_part8<T>(p, C - col, v + 8 * i);
             }
@@ -80,17 +78,25 @@ struct Row {
     }
 };
 
-// A float vector of the channels, `none` where it is not given.
-template <int E, bool TAIL>
+// A float vector of the channels, `none` where it is not given.  Through a buffer of its C
+// values (none at all without a vector), past whose end loads read 0: no branch, so the loads
+// of several vectors are under way together.
+template <int E, Tail TAIL>
 __device__ __forceinline__ void load_vec(const float *p, float none, int l, int L, int C, float (&o)[E])
 {
-    if (p) {
-        Row<F32, E, TAIL> r;
-        r.load((const char *)p, l, L, C, true);
-        r.get(o, l, L, C);
-    } else {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, p ? 4 * C : 0, 0x00020000);
+    const float add = p ? 0.f : none;
+    if constexpr (TAIL == WHOLE) {
 #pragma unroll
-        for (int j = 0; j < E; ++j) o[j] = none;
+        for (int i = 0; i < E / 4; ++i) {
+            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, 4 * col_of<E>(4 * i, l, L), 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[4 * i + e] = __uint_as_float(v[e]) + add;
+        }
+    } else {   // value by value: no access lies partly past the end
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            o[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, 4 * col_of<E>(j, l, L), 0, 0)) + add;
     }
 }
 
@@ -159,13 +165,13 @@ struct RowSum {
 // (one 16-byte access of a 2-byte type) where a row then fits the workgroup, else sixteen.
 struct Layout {
     int E, L, rpb, threads;   // values a thread, threads a row, rows a workgroup
-    bool tail;
+    Tail tail;
 };
 
 inline Layout layout_of(int C, int most, int limit)
 {
     Layout o;
-    o.tail = C % 8 != 0;
+    o.tail = C % 8 == 0 ? WHOLE : C > 8 ? PART : SHORT;
     o.E = (C + 7) / 8 <= limit ? 8 : 16;
     const int n = (C + o.E - 1) / o.E;
     o.L = 1;

@@ -68,7 +68,7 @@ Deal deal_of(uint32_t rows, uint32_t rpg, bool gate, int C)
     return d;
 }
 
-template <typename TS, typename TB, int E, bool TAIL, bool SPLIT>
+template <typename TS, typename TB, int E, Tail TAIL, bool SPLIT>
 __global__ __launch_bounds__(BWD_THREADS) void block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
 {
     __shared__ float red[2][MAX_WAVES][2];
@@ -345,11 +345,10 @@ __global__ __launch_bounds__(FIN_THREADS) void block_norm_bwd_finish_kernel(Bloc
 
 using Kernel = void (*)(BlockNormArgs, int, int, int, int);
 
-template <typename TS, typename TB, int E>
-Kernel kernel_of(bool tail, bool split)
+template <typename TS, typename TB, int E, Tail TAIL>
+Kernel kernel_of(bool split)
 {
-    return tail ? (split ? block_norm_bwd_kernel<TS, TB, E, true, true> : block_norm_bwd_kernel<TS, TB, E, true, false>)
-               : (split ? block_norm_bwd_kernel<TS, TB, E, false, true> : block_norm_bwd_kernel<TS, TB, E, false, false>);
+    return split ? block_norm_bwd_kernel<TS, TB, E, TAIL, true> : block_norm_bwd_kernel<TS, TB, E, TAIL, false>;
 }
 
 template <typename TS, typename TB>
@@ -361,7 +360,9 @@ hipError_t launch_types(BlockNormArgs a, hipStream_t st)
     const bool params = a.dres_scale || a.dpost_w || a.dpost_b || a.dpre_w || a.dpre_b;
     const bool gates = a.dgate && d.split;
     if (!params && !gates) a.part = nullptr;
-    auto k = o.E == 8 ? kernel_of<TS, TB, 8>(o.tail, d.split) : kernel_of<TS, TB, 16>(o.tail, d.split);
+    auto k = o.E == 16 ? (o.tail == WHOLE ? kernel_of<TS, TB, 16, WHOLE>(d.split) : kernel_of<TS, TB, 16, PART>(d.split))
+             : o.tail == WHOLE  ? kernel_of<TS, TB, 8, WHOLE>(d.split)
+             : o.tail == PART ? kernel_of<TS, TB, 8, PART>(d.split) : kernel_of<TS, TB, 8, SHORT>(d.split);
     hipError_t e = launch(k, dim3(d.blocks), dim3(o.threads), 0, st, nullptr, nullptr, a, o.L, o.rpb, d.per, d.gates);
     if (e != hipSuccess || !a.part) return e;
     const int pairs = (a.f != nullptr) + (a.pre != CBR_NORM_NONE);

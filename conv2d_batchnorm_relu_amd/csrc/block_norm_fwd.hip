@@ -14,7 +14,7 @@ using namespace bnorm;
 constexpr int E = 8;   // values a thread (sixteen with their coefficients do not fit 128 registers)
 
 // (v - mean) / std of a row in place; st: (mean, 1/std).
-template <bool TAIL>
+template <Tail TAIL>
 __device__ __forceinline__ void normalise(float (&v)[E], int kind, float eps, int l, int L, int C, RowSum<1> &sum,
                                           float &mean, float &inv)
 {
@@ -38,7 +38,7 @@ __device__ __forceinline__ void normalise(float (&v)[E], int kind, float eps, in
     for (int j = 0; j < E; ++j) v[j] *= inv;
 }
 
-template <typename TS, typename TB, bool TAIL>
+template <typename TS, typename TB, Tail TAIL>
 __global__ __launch_bounds__(1024) void block_norm_fwd_kernel(BlockNormArgs p, int L, int rpb)
 {
     __shared__ float red[2][MAX_WAVES][1];
@@ -116,7 +116,8 @@ hipError_t launch_types(const BlockNormArgs &a, hipStream_t st)
     // As many workgroups as run at once (sixteen waves a CU), each with the same number of rows
     const uint32_t most = 256u * std::max(1u, 1024u / o.threads), turns = (need + most - 1) / most;
     const uint32_t grid = (need + turns - 1) / turns;
-    auto k = o.tail ? block_norm_fwd_kernel<TS, TB, true> : block_norm_fwd_kernel<TS, TB, false>;
+    auto k = o.tail == WHOLE  ? block_norm_fwd_kernel<TS, TB, WHOLE>
+             : o.tail == PART ? block_norm_fwd_kernel<TS, TB, PART> : block_norm_fwd_kernel<TS, TB, SHORT>;
     return launch(k, dim3(grid), dim3(o.threads), 0, st, nullptr, nullptr, a, o.L, o.rpb);
 }
 

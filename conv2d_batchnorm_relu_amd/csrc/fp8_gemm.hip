@@ -394,69 +394,97 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
             af[1][0] = lds_read16<16 * BK>(fa);
             af[1][1] = lds_read16<16 * BK>(fax);
         }
-        f32x4 q[NS];
-        Wide<FB> wb[WIDE ? NS : 1];
-        auto add = [&](int i, int j) __attribute__((always_inline)) {
+        f32x4 q[WIDE ? 2 : 1][NS];
+        auto add = [&](int i, int j, const f32x4 &v) __attribute__((always_inline)) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                acc[i][j][e] = fmaf(BB == 1 ? q[i][e] * t4[BB == 1 ? i : 0][e] : q[i][e], s[j], acc[i][j][e]);
+                acc[i][j][e] = fmaf(BB == 1 ? v[e] * t4[BB == 1 ? i : 0][e] : v[e], s[j], acc[i][j][e]);
         };
-        unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
-            constexpr int J = decltype(jc)::value;
-            lgkm_wait<(J + 1 < MS ? 2 : 0)>();   // all but the next fragment of a
-            if constexpr (J == 0) {
+        auto ready = [&]() __attribute__((always_inline)) {   // b's fragments and the scales
 #pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    after_wait(bf[i][0]);
-                    after_wait(bf[i][1]);
-                }
-#pragma unroll
-                for (int j = 0; j < MS; ++j) after_wait(s[j]);
-                if constexpr (BB == 1) {
-#pragma unroll
-                    for (int i = 0; i < NS; ++i) after_wait(t4[i]);
-                } else {
-                    after_wait(s1);
-#pragma unroll
-                    for (int j = 0; j < MS; ++j) s[j] *= s1;
-                }
+            for (int i = 0; i < NS; ++i) {
+                after_wait(bf[i][0]);
+                after_wait(bf[i][1]);
             }
-            after_wait(af[J % 3][0]);
-            after_wait(af[J % 3][1]);
-            // the next fragment but one, once the products that read its registers are under way
-            auto ahead = [&]() __attribute__((always_inline)) {
-                if constexpr (J + 2 < MS) {
+#pragma unroll
+            for (int j = 0; j < MS; ++j) after_wait(s[j]);
+            if constexpr (BB == 1) {
+#pragma unroll
+                for (int i = 0; i < NS; ++i) after_wait(t4[i]);
+            } else {
+                after_wait(s1);
+#pragma unroll
+                for (int j = 0; j < MS; ++j) s[j] *= s1;
+            }
+        };
+        if constexpr (WIDE) {
+            // Fragment j + 1 is widened, and the products of j - 1 are scaled and added, between
+            // the products of j: four vector instructions to a matrix instruction of 16 cycles.
+            // (One after the other, both waves of a SIMD did the same at the same time: 43 us
+            // for 1024 x 256 x 50176, the matrix unit busy 31% of it.)
+            Wide<FB> wb[NS];
+            Wide<FA> wa[2];
+            lgkm_wait<(MS > 1 ? 2 : 0)>();
+            ready();
+            after_wait(af[0][0]);
+            after_wait(af[0][1]);
+#pragma unroll
+            for (int i = 0; i < NS; ++i) wb[i].set(bf[i][0], bf[i][1]);
+            wa[0].set(af[0][0], af[0][1]);
+            unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int J = decltype(jc)::value;
+                if constexpr (J + 2 < MS) {   // (its registers were widened two turns ago)
                     af[(J + 2) % 3][0] = lds_read16<(J + 2) * 16 * BK>(fa);
                     af[(J + 2) % 3][1] = lds_read16<(J + 2) * 16 * BK>(fax);
                 }
-            };
-            if constexpr (WIDE) {
-                if constexpr (J == 0)
-#pragma unroll
-                    for (int i = 0; i < NS; ++i) wb[i].set(bf[i][0], bf[i][1]);
-                Wide<FA> wa;
-                wa.set(af[J % 3][0], af[J % 3][1]);
-                ahead();
+                if constexpr (J + 1 < MS) {
+                    lgkm_wait<(J + 2 < MS ? 2 : 0)>();
+                    after_wait(af[(J + 1) % 3][0]);
+                    after_wait(af[(J + 1) % 3][1]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int i = 0; i < NS; ++i) {
-                        if (J > 0 && t == 0) add(i, J - 1);
-                        q[i] = product(wb[i].t[t], wa.t[t], t == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : q[i]);
-                    }
-            } else {
+                    for (int i = 0; i < NS; ++i)
+                        q[J % 2][i] = product(wb[i].t[t], wa[J % 2].t[t], t == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : q[J % 2][i]);
+                if constexpr (J + 1 < MS) wa[(J + 1) % 2].set(af[(J + 1) % 3][0], af[(J + 1) % 3][1]);
+                if constexpr (J > 0)
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) add(i, J - 1, q[(J - 1) % 2][i]);
+#pragma unroll
+                for (int u = 0; u < 4 * NS; ++u) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);   // a matrix instruction
+                    __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);   // four of the vector unit
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+#pragma unroll
+            for (int i = 0; i < NS; ++i) add(i, MS - 1, q[(MS - 1) % 2][i]);
+        } else {
+            unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int J = decltype(jc)::value;
+                lgkm_wait<(J + 1 < MS ? 2 : 0)>();   // all but the next fragment of a
+                if constexpr (J == 0) ready();
+                after_wait(af[J % 3][0]);
+                after_wait(af[J % 3][1]);
                 const i32x8 av = join(af[J % 3][0], af[J % 3][1]);
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
-                    if constexpr (J > 0) add(i, J - 1);
-                    q[i] = product<FB, FA>(join(bf[i][0], bf[i][1]), av);
-                    if (i == 0) ahead();
+                    if constexpr (J > 0) add(i, J - 1, q[0][i]);
+                    q[0][i] = product<FB, FA>(join(bf[i][0], bf[i][1]), av);
+                    // the next fragment but one, once the products that read its registers are under way
+                    if constexpr (J + 2 < MS)
+                        if (i == 0) {
+                            af[(J + 2) % 3][0] = lds_read16<(J + 2) * 16 * BK>(fa);
+                            af[(J + 2) % 3][1] = lds_read16<(J + 2) * 16 * BK>(fax);
+                        }
                     __builtin_amdgcn_sched_barrier(0);
                 }
-            }
-        });
+            });
 #pragma unroll
-        for (int i = 0; i < NS; ++i) add(i, MS - 1);
+            for (int i = 0; i < NS; ++i) add(i, MS - 1, q[0][i]);
+        }
         st = st + 1 == NST ? 0 : st + 1;
     }
     // Epilogue: bias (0 without one) and activation (a lower bound: 0, or none), then whole
@@ -673,7 +701,7 @@ struct GemmPlan {
 // The tile and the number of splits with the least expected time, in us.  Measured on one
 // MI355X: a block of k takes `one` with one workgroup on a CU (256 at a time) and `two` with
 // two (512 at a time, 128-tiles), a workgroup's start and end `ends`; joining splits takes
-// 3 us and moves each part at 4 TB/s.  The 256-tile does twice the arithmetic for each byte
+// 4 us and moves each part twice at 4 TB/s.  The 256-tile does twice the arithmetic for each byte
 // that a wave reads from LDS (8192^3: 484 us against 590), the 128-tile divides better (12544 x
 // 512 x 2048: 23 us against 38).
 struct Costs {
@@ -704,15 +732,15 @@ GemmPlan plan_of(const cbr_gemm_shape &s)
     for (const Form form : {TILE128, TILE256}) {
         if (form == TILE256 && s.d_type == CBR_F32) continue;
         const Costs c = form == TILE256 ? (rows ? Costs{2.2, 0., 5.} : Costs{1.95, 0., 5.})
-                        : s.d_type == CBR_F32 ? (rows ? Costs{1.4, 2.6, 3.} : Costs{1.2, 2.0, 3.})
+                        : s.d_type == CBR_F32 ? (rows ? Costs{1.4, 2.45, 3.} : Costs{1.2, 2.1, 3.})
                                               : (rows ? Costs{1.1, 1.25, 3.} : Costs{1.04, 1.15, 3.});
         const int64_t edge = form == TILE256 ? 256 : 128, tiles = up(s.m, edge) * up(s.n, edge);
-        const int64_t most = tiles < 256 ? std::min(256 / tiles, kbs) : 1;
+        const int64_t fit = form == TILE256 ? 256 : 512, most = tiles < fit ? std::min(fit / tiles, kbs) : 1;
         for (int64_t want = 1; want <= most; want += want < 8 ? 1 : 8) {   // see place() for eights
             const int64_t per = up(kbs, want), splits = up(kbs, per), wgs = tiles * splits;
             const double t = wgs <= 256 || form == TILE256 ? up(wgs, 256) * (per * c.one + c.ends)
                                                            : up(wgs, 512) * (per * c.two + c.ends);
-            const double join = splits > 1 ? 3. + (double)splits * s.m * s.n * 8. / 4e6 : 0.;
+            const double join = splits > 1 ? 4. + (double)splits * s.m * s.n * 8. / 4e6 : 0.;
             if (best.splits == 0 || t + join < least) {
                 least = t + join;
                 best.form = form;
@@ -749,7 +777,7 @@ hipError_t launch_formats(const GemmPlan &pl, const GemmArgs &a, hipStream_t st)
     const bool deep = (int64_t)a.tiles_m * a.tiles_n * pl.splits <= 256;
     if (a.d_type == CBR_F32)
         return deep ? launch_tile<4, 2, 2, 4, 4, FA, FB, BB, true>(pl, a, st)
-                    : launch_tile<4, 2, 2, 4, 2, FA, FB, BB, true>(pl, a, st);
+                    : launch_tile<4, 4, 2, 2, 2, FA, FB, BB, true>(pl, a, st);
     return deep ? launch_tile<4, 2, 2, 4, 4, FA, FB, BB, false>(pl, a, st)
                 : launch_tile<4, 2, 2, 4, 2, FA, FB, BB, false>(pl, a, st);
 }

@@ -248,8 +248,8 @@ def test_gemm_nan_and_infinity():
         qa, sa, _, lda = operand(torch.randn(m, 300, generator=g, device="cuda"), "e4m3", 1)
         qb, sb, _, ldb = operand(torch.randn(140, 300, generator=g, device="cuda"), "e4m3", 128)
         sp = cbr.make_gemm_shape(m, 140, 300, d_type=cbr.CBR_F32, relu=True, lda=lda, ldb=ldb)
-        assert cbr.cbr_gemm_fp8_workspace_bytes(sp) == 0
-        run = lambda: (cbr.cbr_gemm_fp8(sp, qa, sa, qb, sb, None, d := torch.empty(m, 140, device="cuda")), d)[1]  # noqa: E731
+        ws = torch.empty(max(16, cbr.cbr_gemm_fp8_workspace_bytes(sp)), dtype=torch.uint8, device="cuda")
+        run = lambda: (cbr.cbr_gemm_fp8(sp, qa, sa, qb, sb, None, d := torch.empty(m, 140, device="cuda"), ws), d)[1]  # noqa: E731
         clean = run()
         qa[3, 299] = 0x7F
         sa[1, 7] = float("inf")

@@ -279,10 +279,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
 {
     constexpr int NW = WM * WN, BM = 16 * MS * WM, BN = 16 * NS * WN;
     constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;   // load instructions a wave, 8 rows each
-    constexpr int PER = LA + LB + 2;                    // and two for the scales
+    constexpr int PER = LA + LB + 1;                    // and one for the scales
     constexpr int STAGE = stage_bytes<BM, BN>(), SCALES = (BM + BN) * BK;
     static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN && NW >= 2, "tile shape");
-    static_assert(64 * NW % BM == 0 && 64 * NW % BN == 0, "a scale's loads cover the tile evenly");
+    static_assert(32 * NW % BM == 0 && 32 * NW % BN == 0, "half the waves load the scales of a, half those of b");
     static_assert(BB == 1 || 128 % (16 * NS) == 0, "a wave's columns lie in one block of b");
     static_assert(NS % 2 == 0, "products in pairs");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -305,8 +305,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         __builtin_amdgcn_make_buffer_rsrc((void *)(p.b + (int64_t)n0 * p.ldb), 0, rows_b * p.ldb, 0x00020000);
     const int lrow = 8 * wave + (lane >> 3);
     const int lchunk = 16 * ((lane & 7) ^ perm(lrow)), lchunk_b = 16 * ((lane & 7) ^ perm_b<WIDE>(lrow));
-    const int sa_at = wave * 64 % BM, sb_at = wave * 64 % BN;
-    const int sb_n = BB == 1 ? rows_b : (rows_b + 127) / 128;
+    // 64 scales a wave: of a the first half of the waves, of b the others
+    const bool a_scales = wave < NW / 2;
+    const int s_at = a_scales ? wave * 64 % BM : (wave - NW / 2) * 64 % BN;
+    const int s_lds = SCALES + (a_scales ? s_at : BM + s_at) * 4;
+    const int s_len = 4 * (a_scales ? rows_a : BB == 1 ? rows_b : (rows_b + 127) / 128);
+    const float *const s_from = a_scales ? p.sa + m0 : p.sb + n0 / BB;
+    const int64_t s_ld = a_scales ? p.M : p.sb_ld;
     auto load = [&](int kb, int st) __attribute__((always_inline)) {
         const int kat = kb * BK + lchunk, kbt = kb * BK + lchunk_b;   // a chunk past K is not read: zeros
         lds_u8 *base = (lds_u8 *)lds + st * STAGE;
@@ -317,13 +322,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
 #pragma unroll
         for (int t = 0; t < LB; ++t)
             buffer_load_lds16(rb, dst + BM * BK + t * NW * 1024, kbt < p.K ? (lrow + t * 8 * NW) * p.ldb + kbt : (int)OOB);
-        // 64 scales a wave; where there are more waves than that, several load the same ones
-        const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc(
-            (void *)(p.sa + (int64_t)kb * p.M + m0), 0, rows_a * 4, 0x00020000);
-        const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc(
-            (void *)(p.sb + (int64_t)kb * p.sb_ld + n0 / BB), 0, sb_n * 4, 0x00020000);
-        buffer_load_lds4(rsa, base + SCALES + sa_at * 4, (sa_at + lane) * 4);
-        buffer_load_lds4(rsb, base + SCALES + BM * 4 + sb_at * 4, (sb_at + lane) * 4);
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void *)(s_from + kb * s_ld), 0, s_len, 0x00020000);
+        buffer_load_lds4(rs, base + s_lds, (s_at + lane) * 4);
     };
 
     f32x4 acc[NS][MS];
@@ -349,9 +349,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         const int kb = kb0 + t;
-        // Block t + NST - 1 takes the place of block t - 1: every wave is past its reads (their
-        // values went into products) when it reaches the barrier.
-        if (t + NST - 1 < turns) load(kb + NST - 1, st == 0 ? NST - 1 : st - 1);
         if (kb + 1 == p.kbs && (p.K & 15)) {
             // the chunk that K ends in: clear what lies past it
             const int kl = p.K - kb * BK, c = kl >> 4, cut = kl & 15;
@@ -394,6 +391,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
             af[1][0] = lds_read16<16 * BK>(fa);
             af[1][1] = lds_read16<16 * BK>(fax);
         }
+        // Block t + NST - 1 takes the place of block t - 1: every wave is past its reads (their
+        // values went into products) when it reaches the barrier.  Issued behind this block's
+        // first reads: before them, the loads' issue held the reads up by 500 cycles a block.
+        if (t + NST - 1 < turns) load(kb + NST - 1, st == 0 ? NST - 1 : st - 1);
         f32x4 q[WIDE ? 2 : 1][NS];
         auto add = [&](int i, int j, const f32x4 &v) __attribute__((always_inline)) {
 #pragma unroll

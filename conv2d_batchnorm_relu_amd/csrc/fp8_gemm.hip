@@ -392,9 +392,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
             af[1][1] = lds_read16<16 * BK>(fax);
         }
         // Block t + NST - 1 takes the place of block t - 1: every wave is past its reads (their
-        // values went into products) when it reaches the barrier.  Issued behind this block's
-        // first reads: before them, the loads' issue held the reads up by 500 cycles a block.
-        if (t + NST - 1 < turns) load(kb + NST - 1, st == 0 ? NST - 1 : st - 1);
+        // values went into products) when it reaches the barrier.  Issued among the products:
+        // before the block's first reads, the loads held them up by 500 cycles a block (8192^3
+        // 484 us, 456 right behind the first reads, 454 here).
+        auto load_ahead = [&]() __attribute__((always_inline)) {
+            if (t + NST - 1 < turns) load(kb + NST - 1, st == 0 ? NST - 1 : st - 1);
+        };
         f32x4 q[WIDE ? 2 : 1][NS];
         auto add = [&](int i, int j, const f32x4 &v) __attribute__((always_inline)) {
 #pragma unroll
@@ -438,6 +441,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
                     af[(J + 2) % 3][0] = lds_read16<(J + 2) * 16 * BK>(fa);
                     af[(J + 2) % 3][1] = lds_read16<(J + 2) * 16 * BK>(fax);
                 }
+                if constexpr (J == MS / 2) load_ahead();
                 if constexpr (J + 1 < MS) {
                     lgkm_wait<(J + 2 < MS ? 2 : 0)>();
                     after_wait(af[(J + 1) % 3][0]);
@@ -470,6 +474,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
                 after_wait(af[J % 3][0]);
                 after_wait(af[J % 3][1]);
                 const i32x8 av = join(af[J % 3][0], af[J % 3][1]);
+                if constexpr (J == 1) load_ahead();
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
                     if constexpr (J > 0) add(i, J - 1, q[0][i]);

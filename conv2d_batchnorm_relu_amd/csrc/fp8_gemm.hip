@@ -695,7 +695,7 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs p, int splits)
 }
 
 // ------------------------------------------------------------------------------ plan
-enum Form { FEW, TILE128, TILE256 };
+enum Form { FEW, TILE64, TILE128, TILE256 };
 
 struct GemmPlan {
     Form form;
@@ -706,10 +706,11 @@ struct GemmPlan {
 
 // The tile and the number of splits with the least expected time, in us.  Measured on one
 // MI355X: a block of k takes `one` with one workgroup on a CU (256 at a time) and `two` with
-// two (512 at a time, 128-tiles), a workgroup's start and end `ends`; joining splits takes
+// two (512 at a time, the smaller tiles), a workgroup's start and end `ends`; joining splits takes
 // 4 us and moves each part twice at 4 TB/s.  The 256-tile does twice the arithmetic for each byte
-// that a wave reads from LDS (8192^3: 484 us against 590), the 128-tile divides better (12544 x
-// 512 x 2048: 23 us against 38).
+// that a wave reads from LDS (8192^3: 456 us against 590), the 128-tile divides better (12544 x
+// 512 x 2048: 23 us against 38), and a lone workgroup takes a block in 0.43 us with a 64-tile, 1.04
+// with a 128-tile (465 x 1252 x 1540: 9 us against 16).
 struct Costs {
     double one, two, ends;
 };
@@ -735,12 +736,13 @@ GemmPlan plan_of(const cbr_gemm_shape &s)
         least = 2. + (double)s.n * s.k / 6.1e6 * (1. + 0.032 * s.m) + (best.splits > 1 ? 3. : 0.);
     }
     const bool rows = s.b_block == 1;
-    for (const Form form : {TILE128, TILE256}) {
+    for (const Form form : {TILE64, TILE128, TILE256}) {
         if (form == TILE256 && s.d_type == CBR_F32) continue;
-        const Costs c = form == TILE256 ? (rows ? Costs{2.2, 0., 5.} : Costs{1.95, 0., 5.})
+        const Costs c = form == TILE64    ? (s.d_type == CBR_F32 ? Costs{0.67, 0.9, 3.} : Costs{0.43, 0.52, 3.})
+                        : form == TILE256 ? (rows ? Costs{2.2, 0., 5.} : Costs{1.95, 0., 5.})
                         : s.d_type == CBR_F32 ? (rows ? Costs{1.4, 2.45, 3.} : Costs{1.2, 2.1, 3.})
                                               : (rows ? Costs{1.1, 1.25, 3.} : Costs{1.04, 1.15, 3.});
-        const int64_t edge = form == TILE256 ? 256 : 128, tiles = up(s.m, edge) * up(s.n, edge);
+        const int64_t edge = form == TILE256 ? 256 : form == TILE128 ? 128 : 64, tiles = up(s.m, edge) * up(s.n, edge);
         const int64_t fit = form == TILE256 ? 256 : 512, most = tiles < fit ? std::min(fit / tiles, kbs) : 1;
         for (int64_t want = 1; want <= most; want += want < 8 ? 1 : 8) {   // see place() for eights
             const int64_t per = up(kbs, want), splits = up(kbs, per), wgs = tiles * splits;
@@ -779,6 +781,9 @@ hipError_t launch_formats(const GemmPlan &pl, const GemmArgs &a, hipStream_t st)
         return launch(k, dim3(a.tiles_n, pl.splits), dim3(64 * SKW), 0, st, nullptr, nullptr, a);
     }
     if (pl.form == TILE256) return launch_tile<8, 4, 2, 4, 2, FA, FB, BB, false>(pl, a, st);
+    if (pl.form == TILE64)
+        return a.d_type == CBR_F32 ? launch_tile<2, 2, 2, 2, 4, FA, FB, BB, true>(pl, a, st)
+                                   : launch_tile<2, 2, 2, 2, 4, FA, FB, BB, false>(pl, a, st);
     // one workgroup a CU: four blocks deep; more: two, and two workgroups share a CU
     const bool deep = (int64_t)a.tiles_m * a.tiles_n * pl.splits <= 256;
     if (a.d_type == CBR_F32)

@@ -56,14 +56,20 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d)
     return (uint32_t)r;
 }
 
-// Eight values of a row at column col, zeros past its end.
+// Eight values of a row at column col, zeros past its end.  The last, partial chunk of a row
+// is loaded as the row's last eight values and moved to the front by settle8, once all loads
+// are out: value by value, each would be waited for.
 template <typename T, bool TAIL>
 __device__ __forceinline__ void load8(const char *row, int64_t col, int64_t cols, bool on, Raw8<T> &r)
 {
-    const char *p = row + col * T::SIZE;
-    if (on && col + (TAIL ? 8 : 1) <= cols) load_raw8<T, TAIL>(p, r);
-    else if (TAIL && on && col < cols) load_part8<T>(p, (int)(cols - col), r);
-    else r = Raw8<T>{};
+    if (!on || col >= cols) r = Raw8<T>{};
+    else if (TAIL && cols < 8) load_part8<T>(row, (int)cols, r);
+    else load_raw8<T, TAIL>(row + (TAIL ? min(col, cols - 8) : col) * T::SIZE, r);
+}
+template <typename T, bool TAIL>
+__device__ __forceinline__ void settle8(int64_t col, int64_t cols, Raw8<T> &r)
+{
+    if (TAIL && cols >= 8) drop8<T>(r, 8 - (int)(cols & 7), col < cols && col + 8 > cols);
 }
 
 // Groups of 128 values of a row: sixteen lanes a group, eight values each.  A workgroup takes
@@ -89,6 +95,7 @@ __global__ __launch_bounds__(NT) void quant_rows_kernel(const char *__restrict__
     for (int u = 0; u < U; ++u) {
         const int64_t row = row0 + u * 16 + sub;
         float v[8], amax = 0.f;
+        settle8<T, TAIL>(col, cols, raw[u]);
         unpack8<T>(raw[u], v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
@@ -125,6 +132,7 @@ __global__ __launch_bounds__(NT) void quant_tile_kernel(const char *__restrict__
 {
     __shared__ float red[4][BLOCK == 1 ? TS : 1];
     __shared__ uint32_t turn[TRANS ? TS * LROW : 1];
+    __shared__ f32x4 groups[BLOCK == 1 ? TS : 1];
     const int64_t ct = blockIdx.x % ctiles, rt = blockIdx.x / ctiles;
     const int cl = threadIdx.x % 16, rl = threadIdx.x / 16, wave = threadIdx.x / 64;
     const int64_t row0 = rt * TS + rl * 8, col = ct * TS + cl * 8;
@@ -138,6 +146,7 @@ __global__ __launch_bounds__(NT) void quant_tile_kernel(const char *__restrict__
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float v[8];
+        settle8<T, TAIL>(col, cols, raw[i]);
         unpack8<T>(raw[i], v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax[e] = fmaxf(amax[e], fabsf(v[e]));
@@ -153,15 +162,23 @@ __global__ __launch_bounds__(NT) void quant_tile_kernel(const char *__restrict__
 #pragma unroll
             for (int e = 0; e < 8; ++e) red[wave][cl * 8 + e] = amax[e];
         __syncthreads();
+        // a thread a column works out its group (two divisions: eight columns in every thread
+        // took 3 us of the smallest call's 8)
+        if (threadIdx.x < TS) {
+            const int c = threadIdx.x;
+            Group<E5M2> w;
+            w.set(fmaxf(fmaxf(red[0][c], red[1][c]), fmaxf(red[2][c], red[3][c])));
+            groups[c] = f32x4{w.c, w.m, w.rm, w.scale};
+            if (ct * TS + c < cols) scale[rt * cols + ct * TS + c] = w.scale;
+        }
+        __syncthreads();
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int c = cl * 8 + e;
-            g[e].set(fmaxf(fmaxf(red[0][c], red[1][c]), fmaxf(red[2][c], red[3][c])));
+            const f32x4 w = groups[cl * 8 + e];
+            g[e].c = w[0];
+            g[e].m = w[1];
+            g[e].rm = w[2];
         }
-        if (rl == 0)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (col + e < cols) scale[rt * cols + col + e] = g[e].scale;
     } else {
         float m = amax[0];
 #pragma unroll

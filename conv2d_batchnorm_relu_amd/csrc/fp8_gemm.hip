@@ -494,10 +494,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         st = st + 1 == NST ? 0 : st + 1;
     }
     // Epilogue: bias (0 without one) and activation (a lower bound: 0, or none), then whole
-    // chunks, or value by value in a tile that N ends in.
+    // chunks, or value by value in the one that N ends in.
     const int nl = n0 + wn * 16 * NS + col_in_wave<WIDE>(0, g, 0);
     const int64_t mw = m0 + wm * 16 * MS + r16;
-    const bool whole = n0 + BN <= p.N, half = p.d_type == CBR_F16;
+    const bool half = p.d_type == CBR_F16;
     const float *bias = p.part ? nullptr : p.bias;
     const float low = p.relu && !p.part ? 0.f : -__builtin_inff();
     f32x4 bv[NS];
@@ -506,7 +506,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         const int n = nl + col_in_wave<WIDE>(i, 0, 0);
         bv[i] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (bias) {
-            if (whole) bv[i] = *(const f32x4 *)(bias + n);
+            if (n + 4 <= p.N) bv[i] = *(const f32x4 *)(bias + n);
             else
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -529,10 +529,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
                 for (int i = 0; i < NS; ++i) {
                     const int c = col_in_wave<WIDE>(i, 0, 0);
                     const f32x4 v = value(i, j);
-                    if (whole) ((LooseF4 *)(o + c))->v = v;
-                    else
+                    if (nl + c + 4 <= p.N) ((LooseF4 *)(o + c))->v = v;
+                    else if (nl + c < p.N)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < 3; ++e)
                             if (nl + c + e < p.N) o[c + e] = v[e];
                 }
     } else {
@@ -546,10 +546,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
                     const f32x4 v = value(i, j), w = value(i + 1, j);
                     const u32x4 r = half ? u32x4{F16::pack(v[0], v[1]), F16::pack(v[2], v[3]), F16::pack(w[0], w[1]), F16::pack(w[2], w[3])}
                                          : u32x4{Bf16::pack(v[0], v[1]), Bf16::pack(v[2], v[3]), Bf16::pack(w[0], w[1]), Bf16::pack(w[2], w[3])};
-                    if (whole) ((Loose16 *)(o + c))->v = r;
-                    else
+                    if (nl + c + 8 <= p.N) ((Loose16 *)(o + c))->v = r;
+                    else if (nl + c < p.N)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
+                        for (int e = 0; e < 7; ++e)
                             if (nl + c + e < p.N) o[c + e] = (uint16_t)(r[e / 2] >> (16 * (e & 1)));
                 }
     }
@@ -706,11 +706,11 @@ struct GemmPlan {
 
 // The tile and the number of splits with the least expected time, in us.  Measured on one
 // MI355X: a block of k takes `one` with one workgroup on a CU (256 at a time) and `two` with
-// two (512 at a time, the smaller tiles), a workgroup's start and end `ends`; joining splits takes
+// two (512 at a time, the smaller tiles), a workgroup's start and end `ends`, the launch 2.3; joining splits takes
 // 4 us and moves each part twice at 4 TB/s.  The 256-tile does twice the arithmetic for each byte
 // that a wave reads from LDS (8192^3: 456 us against 590), the 128-tile divides better (12544 x
-// 512 x 2048: 23 us against 38), and a lone workgroup takes a block in 0.43 us with a 64-tile, 1.04
-// with a 128-tile (465 x 1252 x 1540: 9 us against 16).
+// 512 x 2048: 23 us against 38), and a lone workgroup takes a block in 0.43 us with a 64-tile, 0.68
+// with a 128-tile (465 x 1252 x 1540: 9 us against 16; 65536 x 64 x 64: 7 against 12).
 struct Costs {
     double one, two, ends;
 };
@@ -738,16 +738,16 @@ GemmPlan plan_of(const cbr_gemm_shape &s)
     const bool rows = s.b_block == 1;
     for (const Form form : {TILE64, TILE128, TILE256}) {
         if (form == TILE256 && s.d_type == CBR_F32) continue;
-        const Costs c = form == TILE64    ? (s.d_type == CBR_F32 ? Costs{0.67, 0.9, 3.} : Costs{0.43, 0.52, 3.})
-                        : form == TILE256 ? (rows ? Costs{2.2, 0., 5.} : Costs{1.95, 0., 5.})
-                        : s.d_type == CBR_F32 ? (rows ? Costs{1.4, 2.45, 3.} : Costs{1.2, 2.1, 3.})
-                                              : (rows ? Costs{1.1, 1.25, 3.} : Costs{1.04, 1.15, 3.});
+        const Costs c = form == TILE256  ? (rows ? Costs{2.15, 0., 6.} : Costs{1.76, 0., 6.})
+                        : form == TILE64 ? (s.d_type == CBR_F32 ? Costs{0.67, 0.9, 2.} : Costs{0.43, 0.52, 1.6})
+                        : s.d_type == CBR_F32 ? (rows ? Costs{1.15, 2.15, 3.} : Costs{1.0, 1.9, 3.})
+                                              : (rows ? Costs{0.8, 1.25, 3.} : Costs{0.68, 1.1, 3.});
         const int64_t edge = form == TILE256 ? 256 : form == TILE128 ? 128 : 64, tiles = up(s.m, edge) * up(s.n, edge);
         const int64_t fit = form == TILE256 ? 256 : 512, most = tiles < fit ? std::min(fit / tiles, kbs) : 1;
         for (int64_t want = 1; want <= most; want += want < 8 ? 1 : 8) {   // see place() for eights
             const int64_t per = up(kbs, want), splits = up(kbs, per), wgs = tiles * splits;
-            const double t = wgs <= 256 || form == TILE256 ? up(wgs, 256) * (per * c.one + c.ends)
-                                                           : up(wgs, 512) * (per * c.two + c.ends);
+            const double t = 2.3 + (wgs <= 256 || form == TILE256 ? up(wgs, 256) * (per * c.one + c.ends)
+                                                                  : up(wgs, 512) * (per * c.two + c.ends));
             const double join = splits > 1 ? 4. + (double)splits * s.m * s.n * 8. / 4e6 : 0.;
             if (best.splits == 0 || t + join < least) {
                 least = t + join;

@@ -121,6 +121,20 @@ __device__ __forceinline__ float add_across(float v)
     }
 }
 
+// Sum of v over the lanes of a wave that hold the same channels (lane % L, L <= 64): halves,
+// 16-lane rows, then rotations within a row (by 8, by 4: the lanes 8 apart hold one value by
+// then) and exchanges within quads.  Every lane ends with the same sum as those it was added to.
+__device__ __forceinline__ float add_same(float v, int L)
+{
+    if (L <= 32) v = add_across<5>(v);
+    if (L <= 16) v = add_across<4>(v);
+    if (L <= 8) v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x128, 0xf, 0xf, true));   // row_ror:8
+    if (L <= 4) v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x124, 0xf, 0xf, true));   // row_ror:4
+    if (L <= 2) v = add_across<1>(v);
+    if (L <= 1) v = add_across<0>(v);
+    return v;
+}
+
 // Sums over the L threads of each row, for all rows of the workgroup at once: within a wave
 // (both operands of an addition are the same at both lanes, so every lane holds the same sum),
 // then, for rows of several waves, the waves' sums through LDS in wave order.  Two halves of

@@ -69,10 +69,10 @@ Deal deal_of(uint32_t rows, uint32_t rpg, bool gate, int C)
 }
 
 template <typename TS, typename TB, int E, Tail TAIL, bool SPLIT>
-__global__ __launch_bounds__(BWD_THREADS) void block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
+__global__ __launch_bounds__(BWD_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
 {
     __shared__ float red[2][MAX_WAVES][2];
-    __shared__ float comb[BWD_THREADS * E];
+    __shared__ float comb[2][BWD_THREADS * E];
     RowSum<2> sum{red, L, 0};
     const int C = p.C, l = threadIdx.x % L, sub = threadIdx.x / L;
     const bool hasf = p.f != nullptr, haspre = p.pre != CBR_NORM_NONE, haspost = p.post != CBR_NORM_NONE;
@@ -115,12 +115,11 @@ __global__ __launch_bounds__(BWD_THREADS) void block_norm_bwd_kernel(BlockNormAr
             for (int j = 0; j < E; ++j) cw[j] *= gv[j];
         }
     }
-    float s1[E], s0[E], t1[E], t0[E], g1[SPLIT ? 1 : E], g0[SPLIT ? 1 : E];
+    float s1[E], s0[E], t1[E], t0[E], g1[E], g0[E];   // (g1, g0: !SPLIT)
 #pragma unroll
     for (int j = 0; j < E; ++j) s1[j] = s0[j] = t1[j] = t0[j] = 0.f;
-    if constexpr (!SPLIT)
 #pragma unroll
-        for (int j = 0; j < E; ++j) g1[j] = g0[j] = 0.f;
+    for (int j = 0; j < E; ++j) g1[j] = g0[j] = 0.f;
 
     Row<TS, E, TAIL> dyn, yn;
     Row<TB, E, TAIL> dhn, fn;
@@ -225,31 +224,53 @@ __global__ __launch_bounds__(BWD_THREADS) void block_norm_bwd_kernel(BlockNormAr
         }
     }
     if (!p.part) return;
-    // the workgroup's row groups, added in order, one quantity at a time
-    for (int q = 0; q < 4; ++q) {
-        if (q < 2 ? !hasf : !haspre) continue;
-        __syncthreads();
+    // The workgroup's partial row: a pair of sums at a time, added over the lanes of a wave that
+    // hold the same channels, then over the waves (rows of several waves: over the rows) in order.
+    const int slots = L < 64 ? (int)(blockDim.x >> 6) : rpb, slot = L < 64 ? (int)(threadIdx.x >> 6) : sub;
+    auto leave = [&](int pair, float (&u1)[E], float (&u0)[E]) __attribute__((always_inline)) {
+        if (L < 64) {
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            float v;
-            if constexpr (SPLIT) v = q == 0 ? s1[j] : q == 1 ? s0[j] : q == 2 ? t1[j] : t0[j];
-            else v = q == 0 ? g1[j] : q == 1 ? g0[j] : q == 2 ? t1[j] : t0[j];
-            const int c = col_of<E>(j, l, L);
-            comb[sub * L * E + c] = v;
+            for (int j = 0; j < E; ++j) {
+                u1[j] = add_same(u1[j], L);
+                u0[j] = add_same(u0[j], L);
+            }
+        }
+        float *out = p.part + blockIdx.x * part_ld(C) + 2 * (size_t)pair * C;
+        if (slots == 1) {   // nothing to add
+            if (threadIdx.x < (uint32_t)L) {
+                Row<F32, E, TAIL>::store((char *)out, l, L, C, u1);
+                Row<F32, E, TAIL>::store((char *)(out + C), l, L, C, u0);
+            }
+            return;
         }
         __syncthreads();
-        for (int c = threadIdx.x; c < C; c += blockDim.x) {
-            float v = comb[c];
+        if (L >= 64 || (threadIdx.x & 63) < L)
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+                const int at = slot * L * E + col_of<E>(j, l, L);
+                comb[0][at] = u1[j];
+                comb[1][at] = u0[j];
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * C; i += blockDim.x) {
+            const int q = i >= C, c = i - q * C;
+            const float *from = comb[q] + c;
+            float v = from[0];
             int s = 1;
-            for (; s + 4 <= rpb; s += 4) {   // four reads under way, added in order
-                const float a = comb[s * L * E + c], b = comb[(s + 1) * L * E + c];
-                const float d = comb[(s + 2) * L * E + c], f = comb[(s + 3) * L * E + c];
+            for (; s + 4 <= slots; s += 4) {   // four reads under way, added in order
+                const float a = from[s * L * E], b = from[(s + 1) * L * E];
+                const float d = from[(s + 2) * L * E], f = from[(s + 3) * L * E];
                 v = v + a + b + d + f;
             }
-            for (; s < rpb; ++s) v += comb[s * L * E + c];
-            p.part[blockIdx.x * part_ld(C) + (size_t)q * C + c] = v;
+            for (; s < slots; ++s) v += from[s * L * E];
+            out[(size_t)q * C + c] = v;
         }
+    };
+    if (hasf) {
+        if constexpr (SPLIT) leave(0, s1, s0);
+        else leave(0, g1, g0);
     }
+    if (haspre) leave(1, t1, t0);
 }
 
 // The parameters' gradients from the partial rows, in fp64 and a fixed order.  Blocks
@@ -257,7 +278,8 @@ __global__ __launch_bounds__(BWD_THREADS) void block_norm_bwd_kernel(BlockNormAr
 // partial rows (a wave reads 256 bytes of a row, FIN_UN rows' loads under way together) and
 // are added through LDS in wave order.  (Lane shuffles of fp64 values cost more than the
 // loads: 6.6 us against 4 on the smallest case.)  The blocks after them (dgate of a split
-// gate row): 1024 channels of one gate row each, a thread a channel.
+// gate row): of one gate row, 64 channels shared by the waves in the same way, or 1024 where
+// there are few partial rows, a thread a channel.
 constexpr int FIN_RG = 16, FIN_THREADS = 64 * FIN_RG, FIN_UN = 8;
 
 template <typename TB>
@@ -267,30 +289,42 @@ __global__ __launch_bounds__(FIN_THREADS) void block_norm_bwd_finish_kernel(Bloc
     __shared__ double red[2][FIN_RG][64];
     const int C = p.C;
     if ((int)blockIdx.x >= nparam) {
-        const int tiles = (C + FIN_THREADS - 1) / FIN_THREADS, b = blockIdx.x - nparam;
-        const int gi = b / tiles, c = b % tiles * FIN_THREADS + threadIdx.x;
-        if (c >= C) return;
+        // the gate row's `per` partial rows
+        const bool wide = per >= FIN_RG / 2;
+        const int width = wide ? 64 : FIN_THREADS, tiles = (C + width - 1) / width, b = blockIdx.x - nparam;
+        const int gi = b / tiles, c = b % tiles * width + threadIdx.x % width;
+        const int k0 = wide ? threadIdx.x / 64 : 0, step = wide ? FIN_RG : 1;
         const size_t ld = part_ld(C);
-        const float *row = p.part + (size_t)gi * per * ld + c;
         double s1 = 0., s0 = 0.;
-        int k = 0;
-        for (; k + 4 <= per; k += 4, row += 4 * ld) {
-            float a[4], z[4];
+        if (c < C) {
+            const float *row = p.part + (size_t)gi * per * ld + c;
+            for (int k = k0; k < per; k += 4 * step) {
+                float a[4], z[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                a[u] = row[u * ld];
-                z[u] = row[u * ld + C];
-            }
+                for (int u = 0; u < 4; ++u) {
+                    const size_t at = min(k + u * step, per - 1) * ld;   // past the end: read, not added
+                    a[u] = row[at];
+                    z[u] = row[at + C];
+                }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                s1 += a[u];
-                s0 += z[u];
+                for (int u = 0; u < 4; ++u)
+                    if (k + u * step < per) {
+                        s1 += a[u];
+                        s0 += z[u];
+                    }
             }
         }
-        for (; k < per; ++k, row += ld) {
-            s1 += row[0];
-            s0 += row[C];
+        if (wide) {
+            red[0][k0][threadIdx.x % 64] = s1;
+            red[1][k0][threadIdx.x % 64] = s0;
+            __syncthreads();
+            if (k0 != 0) return;
+            for (int i = 1; i < FIN_RG; ++i) {
+                s1 += red[0][i][threadIdx.x];
+                s0 += red[1][i][threadIdx.x];
+            }
         }
+        if (c >= C) return;
         const double w = p.post_w ? p.post_w[c] : 1.0, pb = p.post_b ? p.post_b[c] : 0.0;
         const double ar = (double)p.alpha * (p.res_scale ? p.res_scale[c] : 1.0);
         store_one<TB>((char *)p.dgate + ((size_t)gi * C + c) * TB::SIZE, (float)(ar * (w * s1 + pb * s0)));
@@ -367,7 +401,8 @@ hipError_t launch_types(BlockNormArgs a, hipStream_t st)
     if (e != hipSuccess || !a.part) return e;
     const int pairs = (a.f != nullptr) + (a.pre != CBR_NORM_NONE);
     const int nparam = params ? pairs * ((a.C + 63) / 64) : 0;
-    const int ngate = gates ? d.blocks / d.per * ((a.C + FIN_THREADS - 1) / FIN_THREADS) : 0;
+    const int width = d.per >= FIN_RG / 2 ? 64 : FIN_THREADS;   // channels of a dgate block, as the kernel has it
+    const int ngate = gates ? d.blocks / d.per * ((a.C + width - 1) / width) : 0;
     return launch(block_norm_bwd_finish_kernel<TB>, dim3(nparam + ngate), dim3(FIN_THREADS), 0, st, nullptr, nullptr, a,
                   d.blocks, d.per, (int)d.split, nparam);
 }

@@ -15,6 +15,7 @@ namespace {
 constexpr int64_t MAX_ROWS = 2147483647;
 constexpr int32_t MAX_CHANNELS = 8192;     // 1024 threads of eight values
 constexpr int64_t MAX_STRIDE = 1 << 23;    // 256 rows of a product's tile stay within 31-bit byte offsets
+constexpr int64_t MAX_GROUPS = 1 << 24;    // workgroups of 256 threads: a launch holds fewer than 2^32 threads
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }   // NULL is aligned
 
@@ -66,8 +67,8 @@ int check_quant(const cbr_quant_shape *s)
     if (s->rows > MAX_ROWS || s->cols > MAX_ROWS) return CBR_E_UNSUPPORTED;
     const int64_t v_cols = s->transpose ? s->rows : s->cols;
     if (s->ldq < v_cols || s->ldq % 16) return CBR_E_SHAPE;
-    // one workgroup for each 16 rows and 128 columns at most
-    if (((s->rows + 15) / 16) * ((s->cols + 127) / 128) > MAX_ROWS) return CBR_E_UNSUPPORTED;
+    // one workgroup for each 64 rows and 128 columns (16 rows only where there are few)
+    if (((s->rows + 63) / 64) * ((s->cols + 127) / 128) >= MAX_GROUPS) return CBR_E_UNSUPPORTED;
     return CBR_OK;
 }
 
@@ -80,8 +81,8 @@ int check_gemm(const cbr_gemm_shape *s)
     if (s->lda < s->k || s->ldb < s->k || s->lda % 16 || s->ldb % 16) return CBR_E_SHAPE;
     if (s->m > MAX_ROWS || s->n > MAX_STRIDE || s->lda > MAX_STRIDE || s->ldb > MAX_STRIDE)
         return CBR_E_UNSUPPORTED;
-    // one workgroup for each 128 x 128 results at most
-    if (((s->m + 127) / 128) * ((s->n + 127) / 128) > MAX_ROWS) return CBR_E_UNSUPPORTED;
+    // workgroups of 256 threads for 64 x 64 results, of 512 for 128 x 128 (one row of tiles: half as many, rounded up)
+    if (((s->m + 63) / 64) * ((s->n + 63) / 64) >= MAX_GROUPS - 1) return CBR_E_UNSUPPORTED;
     return CBR_OK;
 }
 

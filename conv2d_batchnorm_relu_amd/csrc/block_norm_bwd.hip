@@ -21,13 +21,11 @@ using namespace bnorm;
 // Otherwise every group of L threads owns `gates` whole gate rows: it finishes their dgate
 // itself and the partial sums are sum g S1, sum g S0, T1, T0.
 
-// Floats from a partial row (four quantities of C channels) to the next.  The 64 beyond them
-// put the rows of a channel on different memory channels: with a stride of 4 KB (C = 256) the
-// kernel that adds 512 of them took 19 us.
-__host__ __device__ constexpr size_t part_ld(int C) { return 4 * (size_t)C + 64; }
+// Floats from a partial row to the next: four quantities of C channels.
+__host__ __device__ constexpr size_t part_ld(int C) { return 4 * (size_t)C; }
 
 constexpr int BWD_THREADS = 512;
-// Workgroups that run at once: one of 512 threads a CU (155 to 230 registers a thread).  With
+// Workgroups that run at once: one of 512 threads a CU (137 to 256 registers a thread).  With
 // two or three times as many, or with two on a CU at 128 registers, the partial rows and the
 // spilled registers cost more than the waves hide (4096 x 4096: 78 us; 512 workgroups 91, at
 // 128 registers 114, 768 of 256 threads 99).
@@ -68,8 +66,14 @@ Deal deal_of(uint32_t rows, uint32_t rpg, bool gate, int C)
     return d;
 }
 
+// Bound by memory (dy, dh, y, f read once, dx, df written once) where the rows are many, by
+// the latency of two sums over a row and of the next row's loads where they are few: 4096 x
+// 4096 (f32 stream, bf16 branch) 70 us = 4.3 TB/s, 64 x 56 x 56 x 256 with a gate an image 138 us
+// = 4.5 TB/s, of 5.2 that a copy reaches.  Two waves a SIMD are what one workgroup a CU gives: the
+// compiler may use all of the registers that leaves, and is told so.
 template <typename TS, typename TB, int E, Tail TAIL, bool SPLIT>
-__global__ __launch_bounds__(BWD_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
+__global__ __launch_bounds__(BWD_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void
+block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
 {
     __shared__ float red[2][MAX_WAVES][2];
     __shared__ float comb[2][BWD_THREADS * E];
@@ -134,7 +138,7 @@ __global__ __launch_bounds__(BWD_THREADS) __attribute__((amdgpu_waves_per_eu(2, 
         if (on && haspost) qsn = *(const f32x2 *)(p.post_stats + 2 * row);
     };
     // The next row's loads run beside this row's sums; with sixteen values a thread there are
-    // no registers for that (90 to 330 spilled), so a row is loaded when its turn comes.
+    // no registers for that (without it up to 26 are spilled), so a row is loaded when its turn comes.
     constexpr bool AHEAD = E == 8;
     if constexpr (AHEAD) fetch(r0);
     uint32_t left = p.rpg;   // rows left of the current gate row (!SPLIT)

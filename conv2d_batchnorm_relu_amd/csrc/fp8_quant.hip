@@ -7,7 +7,8 @@
 // Markstein's division, q0 + (n - q0 m)(1/m).  A value midway between two 8-bit ones (3/4 of
 // a power of two times the largest, say) is then met exactly and goes to the even one; a
 // product with a rounded reciprocal sends a part of them astray.
-// Bound by memory: 2 or 4 bytes read and 1 written for each value.
+// Bound by memory: 2 or 4 bytes read and 1 written for each value (50176 x 1024 bf16 turned
+// over: 28 us = 5.5 TB/s; 64 x 2048: 2.8 us).
 #include "block_launch.h"
 #include "block_types.h"
 

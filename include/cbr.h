@@ -242,8 +242,8 @@ typedef struct cbr_block_shape {
     float eps_post, eps_pre;
 } cbr_block_shape;
 
-/* Workspace bytes of cbr_block_norm_backward; 0 for an invalid shape.  The forward needs
- * none. */
+/* Workspace bytes of cbr_block_norm_backward, never 0 for a valid shape; 0 for an invalid
+ * one.  The forward needs none.  Calls under way at the same time need one each. */
 size_t cbr_block_norm_workspace_bytes(const cbr_block_shape *shape);
 
 /*
@@ -277,7 +277,8 @@ int cbr_block_norm_forward(const cbr_block_shape *shape, const void *x, const vo
  * dpre_b need no bias, dpost_w and dpre_w no weight and dres_scale no res_scale: where the
  * forward read 1 or 0 the gradient exists all the same.
  * The sums over rows run in a fixed order: fp32 over a workgroup's rows, then fp64.
- * dx may alias dy and df may alias f or dh (same type and place).
+ * dx may alias dy and df may alias f or dh (same type and place); no other output may alias
+ * an input.
  */
 int cbr_block_norm_backward(const cbr_block_shape *shape, const void *dy, const void *dh,
                             const void *y, const void *f,
@@ -302,7 +303,8 @@ int cbr_block_norm_backward(const cbr_block_shape *shape, const void *dy, const 
  * left as they are.  scale: float [ceil(v_cols / 128)][ceil(v_rows / block)], the blocks
  * of 128 columns outermost.  A NaN becomes NaN and does not touch the rest of its group;
  * an infinity makes its group's scale infinite, and the group stands for NaN.
- * rows and cols positive, < 2^31, and fewer than 2^31 groups of 16 rows by 128 columns.
+ * rows and cols positive, < 2^31, and ceil(rows / 64) * ceil(cols / 128) < 2^24
+ * (CBR_E_UNSUPPORTED beyond that).  q and scale may not overlap src or each other.
  */
 typedef struct cbr_quant_shape {
     int64_t rows, cols;             /* of src                                         */
@@ -330,11 +332,12 @@ int cbr_fp8_quantize(const cbr_quant_shape *shape, const void *src, void *q, flo
  *   forward:          a = activations [pixels][C], b = filter [K][C] with b_block 128
  *   data gradient:    a = dy [pixels][K],          b = filter transposed [C][K], b_block 128
  *   weight gradient:  a = dy transposed [K][pixels], b = activations transposed, b_block 1
- * m, n, k positive; m < 2^31, n, lda, ldb <= 2^23 (CBR_E_UNSUPPORTED beyond that); a
- * stride that is too small or no multiple of 16 is CBR_E_SHAPE.
+ * m, n, k positive; m < 2^31, n, lda, ldb <= 2^23 and ceil(m / 64) * ceil(n / 64) <
+ * 2^24 - 1 (CBR_E_UNSUPPORTED beyond that); a stride that is too small or no multiple of
+ * 16 is CBR_E_SHAPE.  d and the workspace may not overlap an operand or each other.
  * The workspace (cbr_gemm_fp8_workspace_bytes, 0 where the shape needs none or is
  * invalid) holds the parts of a long sum that several workgroups share; they are added in
- * a fixed order.
+ * a fixed order.  Calls under way at the same time need one each.
  */
 typedef struct cbr_gemm_shape {
     int64_t m;

@@ -301,6 +301,7 @@ def _q(sp, src=FAKE, q=FAKE, s=FAKE):
     (dict(rows=0), 2), (dict(cols=-1), 2), (dict(ldq=120), 2), (dict(ldq=136), 2), (dict(src_type=3), 7),
     (dict(q_type=0), 7), (dict(block=64), 7), (dict(rows=1 << 31), 3), (dict(cols=1 << 31, ldq=1 << 31), 3),
     (dict(rows=2000000000, cols=1 << 20, ldq=1 << 20), 3), (dict(transpose=True, ldq=16), 2),
+    (dict(rows=1 << 30, cols=1, ldq=16), 3),
 ])
 def test_quantise_refusals(kw, status):
     a = dict(rows=64, cols=128)

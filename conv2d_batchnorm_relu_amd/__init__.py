@@ -318,18 +318,21 @@ class _Call:
     the checks.  These run for every tensor of every call, a dozen of them beside a kernel of a
     few microseconds, so the accepted case is one line; only a refused tensor is looked at
     again to say why."""
-    types = None   # cbr_dtype -> frozenset of torch types, made on the first call
+    types = None   # cbr_dtype -> frozenset of torch types, made on the first call with `torch`
+    torch = None
+    __slots__ = ("where", "dev")
 
     def __init__(self, where, *kinds):
-        import torch
         if _Call.types is None:
+            import torch
+            _Call.torch = torch
             _Call.types = {k: frozenset(getattr(torch, n) for n in v) for k, v in _DTYPES.items()}
         for k in kinds:
             if k not in _BYTES:
                 raise CbrError(_E_VALUE, where)
         self.where = where
-        self.torch = torch
-        self.dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+        cuda = _Call.torch.cuda
+        self.dev = _Call.torch._C._cuda_getDevice() if cuda.is_initialized() else -2
 
     def at(self, t, kind, name, numel):
         """Device address of tensor t of cbr_dtype kind with numel elements at least (None: not
@@ -353,7 +356,8 @@ class _Call:
         """The stream's handle (None: the current one, without the Stream object that
         torch.cuda.current_stream() makes: 2.8 us a call against 0.1)."""
         if stream is None:
-            return self.torch._C._cuda_getCurrentRawStream(self.torch.cuda.current_device())
+            dev = self.dev if self.dev >= 0 else self.torch.cuda.current_device()
+            return self.torch._C._cuda_getCurrentRawStream(dev)
         return _stream(stream)
 
     def workspace(self, workspace):

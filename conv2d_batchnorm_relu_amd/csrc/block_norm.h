@@ -121,18 +121,33 @@ __device__ __forceinline__ float add_across(float v)
     }
 }
 
-// Sum of v over the lanes of a wave that hold the same channels (lane % L, L <= 64): halves,
-// 16-lane rows, then rotations within a row (by 8, by 4: the lanes 8 apart hold one value by
-// then) and exchanges within quads.  Every lane ends with the same sum as those it was added to.
-__device__ __forceinline__ float add_same(float v, int L)
+// One step of the sum over the lanes of a wave that hold the same channels (lane % L): halves
+// (STEP 5), 16-lane rows, then rotations within a row (by 8, by 4: the lanes 8 apart hold one
+// value by then) and exchanges within quads (1, 0).  Every lane ends with the same sum as those
+// it was added to.
+template <int STEP>
+__device__ __forceinline__ float add_same(float v)
 {
-    if (L <= 32) v = add_across<5>(v);
-    if (L <= 16) v = add_across<4>(v);
-    if (L <= 8) v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x128, 0xf, 0xf, true));   // row_ror:8
-    if (L <= 4) v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x124, 0xf, 0xf, true));   // row_ror:4
-    if (L <= 2) v = add_across<1>(v);
-    if (L <= 1) v = add_across<0>(v);
-    return v;
+    constexpr int ROR = STEP == 3 ? 0x128 : 0x124;   // row_ror:8, row_ror:4
+    if constexpr (STEP == 3 || STEP == 2)
+        return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), ROR, 0xf, 0xf, true));
+    else
+        return add_across<STEP>(v);
+}
+
+// All steps for the values of two arrays.  One branch a step: with the branches around each
+// value the kernel was half as long again, and a launch of few rows lasts as long as its
+// instructions take to arrive (some 0.5 us per KB).
+template <int E, int STEP = 5>
+__device__ __forceinline__ void add_same(float (&a)[E], float (&b)[E], int L)
+{
+    if (L > 1 << STEP) return;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        a[j] = add_same<STEP>(a[j]);
+        b[j] = add_same<STEP>(b[j]);
+    }
+    if constexpr (STEP > 0) add_same<E, STEP - 1>(a, b, L);
 }
 
 // Sums over the L threads of each row, for all rows of the workgroup at once: within a wave

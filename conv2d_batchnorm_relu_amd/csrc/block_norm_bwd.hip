@@ -86,12 +86,13 @@ block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
     uint32_t step, turns;
     if constexpr (SPLIT) {
         const uint32_t gi = blockIdx.x / per, part = blockIdx.x % per;
-        const uint64_t first = (uint64_t)gi * p.rpg;
-        const uint64_t a = first + (uint64_t)p.rpg * part / per, b = first + (uint64_t)p.rpg * (part + 1) / per;
+        const uint32_t own = p.rpg / per, more = p.rpg % per;   // the first `more` take one more
+        const uint64_t a = (uint64_t)gi * p.rpg + part * own + min(part, more);
+        const uint32_t mine = own + (part < more);
         r0 = a + sub;
-        r1 = b;
+        r1 = a + mine;
         step = rpb;
-        turns = (uint32_t)((b - a + rpb - 1) / rpb);
+        turns = (mine + rpb - 1) / rpb;
     } else {
         const uint64_t own = (uint64_t)gates * p.rpg;
         r0 = ((uint64_t)blockIdx.x * rpb + sub) * own;
@@ -231,21 +232,23 @@ block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
     // The workgroup's partial row: a pair of sums at a time, added over the lanes of a wave that
     // hold the same channels, then over the waves (rows of several waves: over the rows) in order.
     const int slots = L < 64 ? (int)(blockDim.x >> 6) : rpb, slot = L < 64 ? (int)(threadIdx.x >> 6) : sub;
-    auto leave = [&](int pair, float (&u1)[E], float (&u0)[E]) __attribute__((always_inline)) {
-        if (L < 64) {
+    const int pairs = haspre ? 2 : 1;
+#pragma unroll 1
+    for (int pair = hasf ? 0 : 1; pair < pairs; ++pair) {   // (a loop: the code once)
+        float u1[E], u0[E];
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                u1[j] = add_same(u1[j], L);
-                u0[j] = add_same(u0[j], L);
-            }
+        for (int j = 0; j < E; ++j) {
+            u1[j] = pair ? t1[j] : SPLIT ? s1[j] : g1[j];
+            u0[j] = pair ? t0[j] : SPLIT ? s0[j] : g0[j];
         }
+        if (L < 64) add_same<E>(u1, u0, L);
         float *out = p.part + blockIdx.x * part_ld(C) + 2 * (size_t)pair * C;
         if (slots == 1) {   // nothing to add
             if (threadIdx.x < (uint32_t)L) {
                 Row<F32, E, TAIL>::store((char *)out, l, L, C, u1);
                 Row<F32, E, TAIL>::store((char *)(out + C), l, L, C, u0);
             }
-            return;
+            continue;
         }
         __syncthreads();
         if (L >= 64 || (threadIdx.x & 63) < L)
@@ -269,12 +272,7 @@ block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
             for (; s < slots; ++s) v += from[s * L * E];
             out[(size_t)q * C + c] = v;
         }
-    };
-    if (hasf) {
-        if constexpr (SPLIT) leave(0, s1, s0);
-        else leave(0, g1, g0);
     }
-    if (haspre) leave(1, t1, t0);
 }
 
 // The parameters' gradients from the partial rows, in fp64 and a fixed order.  Blocks

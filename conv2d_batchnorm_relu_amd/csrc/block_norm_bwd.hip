@@ -101,31 +101,6 @@ block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
         turns = (uint32_t)own;
     }
 
-    float cw[E], pw[E];        // alpha r post_w (SPLIT: times g), pre_w
-    {
-        float w[E];
-        load_vec<E, TAIL>(p.res_scale, 1.f, l, L, C, cw);
-        load_vec<E, TAIL>(p.post_w, 1.f, l, L, C, w);
-        load_vec<E, TAIL>(p.pre_w, 1.f, l, L, C, pw);
-#pragma unroll
-        for (int j = 0; j < E; ++j) cw[j] *= p.alpha * w[j];
-    }
-    Row<TB, E, TAIL> graw;
-    if constexpr (SPLIT) {
-        if (p.gate) {
-            float gv[E];
-            graw.load((const char *)p.gate + (uint64_t)(blockIdx.x / per) * C * TB::SIZE, l, L, C, true);
-            graw.get(gv, l, L, C);
-#pragma unroll
-            for (int j = 0; j < E; ++j) cw[j] *= gv[j];
-        }
-    }
-    float s1[E], s0[E], t1[E], t0[E], g1[E], g0[E];   // (g1, g0: !SPLIT)
-#pragma unroll
-    for (int j = 0; j < E; ++j) s1[j] = s0[j] = t1[j] = t0[j] = 0.f;
-#pragma unroll
-    for (int j = 0; j < E; ++j) g1[j] = g0[j] = 0.f;
-
     Row<TS, E, TAIL> dyn, yn;
     Row<TB, E, TAIL> dhn, fn;
     f32x2 psn = {0.f, 0.f}, qsn = {0.f, 0.f};
@@ -138,10 +113,34 @@ block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
         if (on && haspre) psn = *(const f32x2 *)(p.pre_stats + 2 * row);
         if (on && haspost) qsn = *(const f32x2 *)(p.post_stats + 2 * row);
     };
-    // The next row's loads run beside this row's sums; with sixteen values a thread there are
-    // no registers for that (without it up to 26 are spilled), so a row is loaded when its turn comes.
+    // The first row, the gate and the vectors are asked for together, and a row's loads run
+    // beside the sums of the row before it; with sixteen values a thread there are no registers
+    // for that (up to 160 spilled), so a row is loaded when its turn comes.
+    Row<TB, E, TAIL> graw;
     constexpr bool AHEAD = E == 8;
     if constexpr (AHEAD) fetch(r0);
+    if constexpr (SPLIT)
+        graw.load((const char *)p.gate + (uint64_t)(blockIdx.x / per) * C * TB::SIZE, l, L, C, p.gate != nullptr);
+    float cw[E], pw[E];        // alpha r post_w (SPLIT: times g), pre_w
+    {
+        float w[E];
+        load_vec<E, TAIL>(p.res_scale, 1.f, l, L, C, cw);
+        load_vec<E, TAIL>(p.post_w, 1.f, l, L, C, w);
+        load_vec<E, TAIL>(p.pre_w, 1.f, l, L, C, pw);
+#pragma unroll
+        for (int j = 0; j < E; ++j) cw[j] *= p.alpha * w[j];
+        if (SPLIT && p.gate) {
+            graw.get(w, l, L, C);
+#pragma unroll
+            for (int j = 0; j < E; ++j) cw[j] *= w[j];
+        }
+    }
+    float s1[E], s0[E], t1[E], t0[E], g1[E], g0[E];   // (g1, g0: !SPLIT)
+#pragma unroll
+    for (int j = 0; j < E; ++j) s1[j] = s0[j] = t1[j] = t0[j] = 0.f;
+#pragma unroll
+    for (int j = 0; j < E; ++j) g1[j] = g0[j] = 0.f;
+
     uint32_t left = p.rpg;   // rows left of the current gate row (!SPLIT)
     for (uint32_t t = 0; t < turns; ++t) {
         const uint64_t row = r0 + (uint64_t)t * step;

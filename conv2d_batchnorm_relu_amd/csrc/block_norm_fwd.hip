@@ -45,6 +45,18 @@ __global__ __launch_bounds__(1024) void block_norm_fwd_kernel(BlockNormArgs p, i
     __shared__ float red[2][MAX_WAVES][1];
     RowSum<1> sum{red, L, 0};
     const int C = p.C, l = threadIdx.x % L, sub = threadIdx.x / L;
+    const uint32_t step = gridDim.x * rpb;
+    // every thread of the workgroup takes the same number of turns (the sums may hold a barrier)
+    const uint32_t turns = (p.rows - blockIdx.x * rpb + step - 1) / step;   // blockIdx.x * rpb < rows
+    Row<TS, E, TAIL> xn;
+    Row<TB, E, TAIL> fn;
+    auto fetch = [&](uint64_t row) __attribute__((always_inline)) {
+        const bool on = row < p.rows;
+        xn.load((const char *)p.x + row * C * TS::SIZE, l, L, C, on);
+        fn.load((const char *)p.f + row * C * TB::SIZE, l, L, C, on && p.f);
+    };
+    uint64_t row = (uint64_t)blockIdx.x * rpb + sub;
+    fetch(row);   // with the vectors: one latency of memory
     // y = x + g (cw nhat + cb), h = pw yhat + pb
     float cw[E], cb[E], pw[E], pb[E];
     {
@@ -60,19 +72,6 @@ __global__ __launch_bounds__(1024) void block_norm_fwd_kernel(BlockNormArgs p, i
     }
     load_vec<E, TAIL>(p.pre_w, 1.f, l, L, C, pw);
     load_vec<E, TAIL>(p.pre_b, 0.f, l, L, C, pb);
-
-    const uint32_t step = gridDim.x * rpb;
-    // every thread of the workgroup takes the same number of turns (the sums may hold a barrier)
-    const uint32_t turns = (p.rows - blockIdx.x * rpb + step - 1) / step;   // blockIdx.x * rpb < rows
-    Row<TS, E, TAIL> xn;
-    Row<TB, E, TAIL> fn;
-    auto fetch = [&](uint64_t row) __attribute__((always_inline)) {
-        const bool on = row < p.rows;
-        xn.load((const char *)p.x + row * C * TS::SIZE, l, L, C, on);
-        fn.load((const char *)p.f + row * C * TB::SIZE, l, L, C, on && p.f);
-    };
-    uint64_t row = (uint64_t)blockIdx.x * rpb + sub;
-    fetch(row);
     for (uint32_t t = 0; t < turns; ++t, row += step) {
         float v[E], y[E];
         xn.get(y, l, L, C);

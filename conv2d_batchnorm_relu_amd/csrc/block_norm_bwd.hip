@@ -76,7 +76,8 @@ __global__ __launch_bounds__(BWD_THREADS) __attribute__((amdgpu_waves_per_eu(2, 
 block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
 {
     __shared__ float red[2][MAX_WAVES][2];
-    __shared__ float comb[2][BWD_THREADS * E];
+    constexpr int COMB = BWD_THREADS * E;
+    __shared__ float comb[E > 8 ? 1 : 4 * COMB];   // (sixteen values a thread: a row takes the whole workgroup)
     RowSum<2> sum{red, L, 0};
     const int C = p.C, l = threadIdx.x % L, sub = threadIdx.x / L;
     const bool hasf = p.f != nullptr, haspre = p.pre != CBR_NORM_NONE, haspost = p.post != CBR_NORM_NONE;
@@ -231,9 +232,10 @@ block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
     // The workgroup's partial row: a pair of sums at a time, added over the lanes of a wave that
     // hold the same channels, then over the waves (rows of several waves: over the rows) in order.
     const int slots = L < 64 ? (int)(blockDim.x >> 6) : rpb, slot = L < 64 ? (int)(threadIdx.x >> 6) : sub;
-    const int pairs = haspre ? 2 : 1;
+    const int first = hasf ? 0 : 1, pairs = haspre ? 2 : 1;
+    float *const out = p.part + blockIdx.x * part_ld(C);
 #pragma unroll 1
-    for (int pair = hasf ? 0 : 1; pair < pairs; ++pair) {   // (a loop: the code once)
+    for (int pair = first; pair < pairs; ++pair) {   // (a loop: the code once)
         float u1[E], u0[E];
 #pragma unroll
         for (int j = 0; j < E; ++j) {
@@ -241,36 +243,34 @@ block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
             u0[j] = pair ? t0[j] : SPLIT ? s0[j] : g0[j];
         }
         if (L < 64) add_same<E>(u1, u0, L);
-        float *out = p.part + blockIdx.x * part_ld(C) + 2 * (size_t)pair * C;
-        if (slots == 1) {   // nothing to add
+        if (E > 8 || slots == 1) {   // nothing to add
             if (threadIdx.x < (uint32_t)L) {
-                Row<F32, E, TAIL>::store((char *)out, l, L, C, u1);
-                Row<F32, E, TAIL>::store((char *)(out + C), l, L, C, u0);
+                Row<F32, E, TAIL>::store((char *)(out + 2 * (size_t)pair * C), l, L, C, u1);
+                Row<F32, E, TAIL>::store((char *)(out + (2 * (size_t)pair + 1) * C), l, L, C, u0);
             }
-            continue;
-        }
-        __syncthreads();
-        if (L >= 64 || (threadIdx.x & 63) < L)
+        } else if (L >= 64 || (threadIdx.x & 63) < L) {
 #pragma unroll
             for (int j = 0; j < E; ++j) {
                 const int at = slot * L * E + col_of<E>(j, l, L);
-                comb[0][at] = u1[j];
-                comb[1][at] = u0[j];
+                comb[2 * pair * COMB + at] = u1[j];
+                comb[(2 * pair + 1) * COMB + at] = u0[j];
             }
-        __syncthreads();
-        for (int i = threadIdx.x; i < 2 * C; i += blockDim.x) {
-            const int q = i >= C, c = i - q * C;
-            const float *from = comb[q] + c;
-            float v = from[0];
-            int s = 1;
-            for (; s + 4 <= slots; s += 4) {   // four reads under way, added in order
-                const float a = from[s * L * E], b = from[(s + 1) * L * E];
-                const float d = from[(s + 2) * L * E], f = from[(s + 3) * L * E];
-                v = v + a + b + d + f;
-            }
-            for (; s < slots; ++s) v += from[s * L * E];
-            out[(size_t)q * C + c] = v;
         }
+    }
+    if (E > 8 || slots == 1) return;
+    __syncthreads();
+    for (int i = threadIdx.x + 2 * first * C; i < 2 * pairs * C; i += blockDim.x) {
+        const int q = (i >= C) + (i >= 2 * C) + (i >= 3 * C);
+        const float *from = comb + q * COMB + (i - q * C);
+        float v = from[0];
+        int s = 1;
+        for (; s + 4 <= slots; s += 4) {   // four reads under way, added in order
+            const float a = from[s * L * E], b = from[(s + 1) * L * E];
+            const float d = from[(s + 2) * L * E], f = from[(s + 3) * L * E];
+            v = v + a + b + d + f;
+        }
+        for (; s < slots; ++s) v += from[s * L * E];
+        out[i] = v;
     }
 }
 
@@ -294,7 +294,7 @@ __global__ __launch_bounds__(FIN_THREADS) void block_norm_bwd_finish_kernel(Bloc
         const bool wide = per >= FIN_RG / 2;
         const int width = wide ? 64 : FIN_THREADS, tiles = (C + width - 1) / width, b = blockIdx.x - nparam;
         const int gi = b / tiles, c = b % tiles * width + threadIdx.x % width;
-        const int k0 = wide ? threadIdx.x / 64 : 0, step = wide ? FIN_RG : 1;
+        const int k0 = wide ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0, step = wide ? FIN_RG : 1;
         const size_t ld = part_ld(C);
         double s1 = 0., s0 = 0.;
         if (c < C) {
@@ -334,7 +334,8 @@ __global__ __launch_bounds__(FIN_THREADS) void block_norm_bwd_finish_kernel(Bloc
     const bool hasf = p.f != nullptr, haspre = p.pre != CBR_NORM_NONE;
     // which pair: the post norm's S1, S0 or the pre norm's T1, T0 (those that exist)
     const bool post = hasf && (!haspre || blockIdx.x % 2 == 0);
-    const int c = (hasf && haspre ? blockIdx.x / 2 : blockIdx.x) * 64 + threadIdx.x % 64, rg = threadIdx.x / 64;
+    const int c = (hasf && haspre ? blockIdx.x / 2 : blockIdx.x) * 64 + threadIdx.x % 64;
+    const int rg = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);   // the addresses' arithmetic is scalar
     const bool weigh = post && split && p.gate;
     double s1 = 0., s0 = 0.;
     if (c < C) {

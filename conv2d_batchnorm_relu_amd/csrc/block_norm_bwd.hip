@@ -9,6 +9,8 @@
 //   T1 = sum dh yhat, T0 = sum dh:  dw' = T1, db' = T0.
 // The sums stay in registers over a workgroup's rows and leave as one partial row; a second
 // kernel adds the partial rows in fp64.
+#include <type_traits>
+
 #include "block_norm.h"
 
 namespace cbr {
@@ -281,8 +283,16 @@ block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
 // loads: 6.6 us against 4 on the smallest case.)  The blocks after them (dgate of a split
 // gate row): of one gate row, 64 channels shared by the waves in the same way, or 1024 where
 // there are few partial rows, a thread a channel.
+// The parameter vectors are read through buffers whose length says what exists, so without
+// branches and beside the sums' loads.
 constexpr int FIN_RG = 16, FIN_THREADS = 64 * FIN_RG, FIN_UN = 8;
 
+// Value c of n floats at p (p NULL or c past the end: `none`).
+__device__ __forceinline__ float float_at(const float *p, int n, int c, float none)
+{
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, p ? 4 * n : 0, 0x00020000);
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, 4 * c, 0, 0)) + (p ? 0.f : none);
+}
 template <typename TB>
 __global__ __launch_bounds__(FIN_THREADS) void block_norm_bwd_finish_kernel(BlockNormArgs p, int blocks, int per,
                                                                             int split, int nparam)
@@ -297,6 +307,8 @@ __global__ __launch_bounds__(FIN_THREADS) void block_norm_bwd_finish_kernel(Bloc
         const int k0 = wide ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0, step = wide ? FIN_RG : 1;
         const size_t ld = part_ld(C);
         double s1 = 0., s0 = 0.;
+        const float w = float_at(p.post_w, C, c, 1.f), pb = float_at(p.post_b, C, c, 0.f);
+        const float res = float_at(p.res_scale, C, c, 1.f);
         if (c < C) {
             const float *row = p.part + (size_t)gi * per * ld + c;
             for (int k = k0; k < per; k += 4 * step) {
@@ -326,9 +338,8 @@ __global__ __launch_bounds__(FIN_THREADS) void block_norm_bwd_finish_kernel(Bloc
             }
         }
         if (c >= C) return;
-        const double w = p.post_w ? p.post_w[c] : 1.0, pb = p.post_b ? p.post_b[c] : 0.0;
-        const double ar = (double)p.alpha * (p.res_scale ? p.res_scale[c] : 1.0);
-        store_one<TB>((char *)p.dgate + ((size_t)gi * C + c) * TB::SIZE, (float)(ar * (w * s1 + pb * s0)));
+        const double ar = (double)p.alpha * res;
+        store_one<TB>((char *)p.dgate + ((size_t)gi * C + c) * TB::SIZE, (float)(ar * ((double)w * s1 + (double)pb * s0)));
         return;
     }
     const bool hasf = p.f != nullptr, haspre = p.pre != CBR_NORM_NONE;
@@ -337,27 +348,38 @@ __global__ __launch_bounds__(FIN_THREADS) void block_norm_bwd_finish_kernel(Bloc
     const int c = (hasf && haspre ? blockIdx.x / 2 : blockIdx.x) * 64 + threadIdx.x % 64;
     const int rg = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);   // the addresses' arithmetic is scalar
     const bool weigh = post && split && p.gate;
+    const float w = float_at(p.post_w, C, c, 1.f), pb = float_at(p.post_b, C, c, 0.f);
+    const float res = float_at(p.res_scale, C, c, 1.f);
     double s1 = 0., s0 = 0.;
-    if (c < C) {
+    auto add = [&](auto un) __attribute__((always_inline)) {   // `un` partial rows at a time
+        constexpr int UN = decltype(un)::value;
         const float *rows = p.part + (post ? 0 : 2 * (size_t)C) + c;
-        for (int b0 = rg; b0 < blocks; b0 += FIN_RG * FIN_UN) {
-            float a[FIN_UN], z[FIN_UN];
-            uint32_t g[FIN_UN];   // as loaded: converted here, each would be waited for
+        for (int b0 = rg; b0 < blocks; b0 += FIN_RG * UN) {
+            float a[UN], z[UN];
+            uint32_t g[UN];
 #pragma unroll
-            for (int u = 0; u < FIN_UN; ++u) {
+            for (int u = 0; u < UN; ++u) {
                 const int b = min(b0 + u * FIN_RG, blocks - 1);   // past the end: read, not added
                 a[u] = rows[b * part_ld(C)];
                 z[u] = rows[b * part_ld(C) + C];
-                if (weigh) g[u] = load_bits<TB>((const char *)p.gate + ((size_t)(b / per) * C + c) * TB::SIZE);
             }
+            if (weigh)
 #pragma unroll
-            for (int u = 0; u < FIN_UN; ++u)
+                for (int u = 0; u < UN; ++u)
+                    g[u] = load_bits<TB>((const char *)p.gate +
+                                         ((size_t)(min(b0 + u * FIN_RG, blocks - 1) / per) * C + c) * TB::SIZE);
+#pragma unroll
+            for (int u = 0; u < UN; ++u)
                 if (b0 + u * FIN_RG < blocks) {
-                    const float gv = weigh ? to_float<TB>(g[u]) : 1.f;
-                    s1 += (double)gv * a[u];
-                    s0 += (double)gv * z[u];
+                    const double gv = weigh ? to_float<TB>(g[u]) : 1.f;
+                    s1 += gv * a[u];
+                    s0 += gv * z[u];
                 }
         }
+    };
+    if (c < C) {
+        if (blocks > FIN_RG) add(std::integral_constant<int, FIN_UN>{});
+        else add(std::integral_constant<int, 1>{});
     }
     red[0][rg][threadIdx.x % 64] = s1;
     red[1][rg][threadIdx.x % 64] = s0;
@@ -368,9 +390,8 @@ __global__ __launch_bounds__(FIN_THREADS) void block_norm_bwd_finish_kernel(Bloc
         s0 += red[1][i][threadIdx.x];
     }
     if (post) {
-        const double w = p.post_w ? p.post_w[c] : 1.0, pb = p.post_b ? p.post_b[c] : 0.0;
-        const double r = p.res_scale ? p.res_scale[c] : 1.0, al = p.alpha;
-        if (p.dres_scale) p.dres_scale[c] = (float)(al * (w * s1 + pb * s0));
+        const double r = res, al = p.alpha;
+        if (p.dres_scale) p.dres_scale[c] = (float)(al * ((double)w * s1 + (double)pb * s0));
         if (p.dpost_w) p.dpost_w[c] = (float)(al * r * s1);
         if (p.dpost_b) p.dpost_b[c] = (float)(al * r * s0);
     } else {

@@ -29,8 +29,8 @@ __host__ __device__ constexpr size_t part_ld(int C) { return 4 * (size_t)C; }
 constexpr int BWD_THREADS = 512;
 // Workgroups that run at once: one of 512 threads a CU (137 to 256 registers a thread).  With
 // two or three times as many, or with two on a CU at 128 registers, the partial rows and the
-// spilled registers cost more than the waves hide (4096 x 4096: 78 us; 512 workgroups 91, at
-// 128 registers 114, 768 of 256 threads 99).
+// spilled registers cost more than the waves hide (4096 x 4096, when this was chosen: 78 us; 512
+// workgroups 91, at 128 registers 114, 768 of 256 threads 99).
 constexpr int BWD_BLOCKS = 256;
 
 struct Deal {

@@ -710,11 +710,12 @@ struct GemmPlan {
 
 // The tile and the number of splits with the least expected time, in us.  Measured on one
 // MI355X: a block of k takes `one` with one workgroup on a CU (256 at a time) and `two` with
-// two (512 at a time, the smaller tiles), a workgroup's start and end `ends`, the launch 2.3; joining splits takes
-// 4 us and moves each part twice at 4 TB/s.  The 256-tile does twice the arithmetic for each byte
-// that a wave reads from LDS (8192^3: 456 us against 590), the 128-tile divides better (12544 x
-// 512 x 2048: 23 us against 38), and a lone workgroup takes a block in 0.43 us with a 64-tile, 0.68
-// with a 128-tile (465 x 1252 x 1540: 9 us against 16; 65536 x 64 x 64: 7 against 12).
+// two (512 at a time, the smaller tiles), a workgroup's start and end `ends`, the launch 2.3;
+// joining splits takes 4 us and moves each part twice at 4 TB/s.  The 256-tile does twice the
+// arithmetic for each byte that a wave reads from LDS (8192^3: 456 us against 590), the
+// 128-tile divides better (12544 x 512 x 2048: 23 us against 38), and a lone workgroup takes a
+// block in 0.43 us with a 64-tile, 0.68 with a 128-tile (465 x 1252 x 1540: 9 us against 16;
+// 65536 x 64 x 64: 7 against 12).
 struct Costs {
     double one, two, ends;
 };
@@ -766,7 +767,7 @@ GemmPlan plan_of(const cbr_gemm_shape &s)
 }
 
 template <int MS, int NS, int WM, int WN, int NST, int FA, int FB, int BB, bool WIDE>
-hipError_t launch_tile(const GemmPlan &pl, const GemmArgs &a, hipStream_t st)
+hipError_t launch_tile(const GemmArgs &a, hipStream_t st)
 {
     auto k = gemm_tile_kernel<MS, NS, WM, WN, NST, FA, FB, BB, WIDE>;
     constexpr int lds = NST * stage_bytes<16 * MS * WM, 16 * NS * WN>();
@@ -784,17 +785,17 @@ hipError_t launch_formats(const GemmPlan &pl, const GemmArgs &a, hipStream_t st)
                  : pl.ms == 2 ? gemm_few_kernel<2, FA, FB, BB> : gemm_few_kernel<4, FA, FB, BB>;
         return launch(k, dim3(a.tiles_n, pl.splits), dim3(64 * SKW), 0, st, nullptr, nullptr, a);
     }
-    if (pl.form == TILE256) return launch_tile<8, 4, 2, 4, 2, FA, FB, BB, false>(pl, a, st);
+    if (pl.form == TILE256) return launch_tile<8, 4, 2, 4, 2, FA, FB, BB, false>(a, st);
     if (pl.form == TILE64)
-        return a.d_type == CBR_F32 ? launch_tile<2, 2, 2, 2, 4, FA, FB, BB, true>(pl, a, st)
-                                   : launch_tile<2, 2, 2, 2, 4, FA, FB, BB, false>(pl, a, st);
+        return a.d_type == CBR_F32 ? launch_tile<2, 2, 2, 2, 4, FA, FB, BB, true>(a, st)
+                                   : launch_tile<2, 2, 2, 2, 4, FA, FB, BB, false>(a, st);
     // one workgroup a CU: four blocks deep; more: two, and two workgroups share a CU
     const bool deep = (int64_t)a.tiles_m * a.tiles_n * pl.splits <= 256;
     if (a.d_type == CBR_F32)
-        return deep ? launch_tile<4, 2, 2, 4, 4, FA, FB, BB, true>(pl, a, st)
-                    : launch_tile<4, 4, 2, 2, 2, FA, FB, BB, true>(pl, a, st);
-    return deep ? launch_tile<4, 2, 2, 4, 4, FA, FB, BB, false>(pl, a, st)
-                : launch_tile<4, 2, 2, 4, 2, FA, FB, BB, false>(pl, a, st);
+        return deep ? launch_tile<4, 2, 2, 4, 4, FA, FB, BB, true>(a, st)
+                    : launch_tile<4, 4, 2, 2, 2, FA, FB, BB, true>(a, st);
+    return deep ? launch_tile<4, 2, 2, 4, 4, FA, FB, BB, false>(a, st)
+                : launch_tile<4, 2, 2, 4, 2, FA, FB, BB, false>(a, st);
 }
 
 }  // namespace

@@ -124,7 +124,18 @@ block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
     if constexpr (AHEAD) fetch(r0);
     if constexpr (SPLIT)
         graw.load((const char *)p.gate + (uint64_t)(blockIdx.x / per) * C * TB::SIZE, l, L, C, p.gate != nullptr);
-    float cw[E], pw[E];        // alpha r post_w (SPLIT: times g), pre_w
+    // alpha r post_w (SPLIT: times g), pre_w, and for whole gate rows' dgate alpha r post_b (sixteen
+    // values a thread: loaded when a gate row ends, there are no registers for them)
+    constexpr bool KEEP = !SPLIT && E == 8;
+    float cw[E], pw[E], cb[KEEP ? E : 1];
+    auto load_cb = [&](float(&o)[E]) __attribute__((always_inline)) {
+        float v[E];
+        load_vec<E, TAIL>(p.post_b, 0.f, l, L, C, o);
+        load_vec<E, TAIL>(p.res_scale, 1.f, l, L, C, v);
+#pragma unroll
+        for (int j = 0; j < E; ++j) o[j] *= p.alpha * v[j];
+    };
+    if constexpr (KEEP) load_cb(cb);
     {
         float w[E];
         load_vec<E, TAIL>(p.res_scale, 1.f, l, L, C, cw);
@@ -211,12 +222,15 @@ block_norm_bwd_kernel(BlockNormArgs p, int L, int rpb, int per, int gates)
                 if (--left == 0) {   // the gate row is done
                     left = p.rpg;
                     if (on && p.dgate) {
-                        float w[E], r[E], pb[E], o[E];
-                        load_vec<E, TAIL>(p.post_w, 1.f, l, L, C, w);
-                        load_vec<E, TAIL>(p.post_b, 0.f, l, L, C, pb);
-                        load_vec<E, TAIL>(p.res_scale, 1.f, l, L, C, r);
+                        float o[E];
 #pragma unroll
-                        for (int j = 0; j < E; ++j) o[j] = p.alpha * r[j] * fmaf(w[j], s1[j], pb[j] * s0[j]);
+                        for (int j = 0; j < E; ++j) o[j] = cw[j] * s1[j];
+                        if (p.post_b) {
+                            float b[E];
+                            if constexpr (!KEEP) load_cb(b);
+#pragma unroll
+                            for (int j = 0; j < E; ++j) o[j] = fmaf(KEEP ? cb[KEEP ? j : 0] : b[j], s0[j], o[j]);
+                        }
                         Row<TB, E, TAIL>::store((char *)p.dgate + (uint64_t)((uint32_t)row / p.rpg) * C * TB::SIZE, l,
                                                L, C, o);
                     }

@@ -76,7 +76,8 @@ int check_gemm(const cbr_gemm_shape *s)
 {
     if (!s) return CBR_E_NULL;
     if (s->m <= 0 || s->n <= 0 || s->k <= 0) return CBR_E_SHAPE;
-    if (!fp8_type(s->a_type) || !fp8_type(s->b_type) || !float_type(s->d_type) || (s->b_block != 1 && s->b_block != 128))
+    if (!fp8_type(s->a_type) || !fp8_type(s->b_type) || !float_type(s->d_type) || (s->b_block != 1 && s->b_block != 128) ||
+        (s->short_sums && s->d_type == CBR_F32))
         return CBR_E_VALUE;
     if (s->lda < s->k || s->ldb < s->k || s->lda % 16 || s->ldb % 16) return CBR_E_SHAPE;
     if (s->m > MAX_ROWS || s->n > MAX_STRIDE || s->lda > MAX_STRIDE || s->ldb > MAX_STRIDE)

@@ -9,13 +9,15 @@
 // product asks of that order.
 //
 // Two ways to sum a block:
-//   * v_mfma_f32_16x16x128_f8f6f4, one instruction for the block, 16-bit outputs.  It aligns
-//     the eight products of each 8 consecutive k to the largest of them and keeps 13 bits
-//     below its leading one (measured; between eights it adds in fp32).  On normal values that
-//     is 1.3e-5 of the result's norm, 130 times below the rounding to bf16 and 16 below f16.
 //   * operands widened to bf16 (exactly) and four v_mfma_f32_16x16x32_bf16, whose sums are
-//     fp32 throughout (same probe), at half the rate: fp32 outputs, and few rows, where
-//     reading b bounds the call.
+//     fp32 throughout (measured): every call that does not ask for short sums.
+//   * v_mfma_f32_16x16x128_f8f6f4, one instruction for the block at twice the rate, for 16-bit
+//     outputs of callers that ask for short sums.  It aligns the eight products of each 8
+//     consecutive k to the largest of them and keeps 13 bits below its leading one (measured;
+//     between eights it adds in fp32).  On normally distributed values that is 1.4e-5 of the
+//     result's norm, but products that cancel within an eight take the small ones with them,
+//     so it is the caller's choice and never the default.
+//     (The few-rows form, bound by reading b, sums in fp32 in any case.)
 #include <type_traits>
 
 #include "block_launch.h"
@@ -250,33 +252,34 @@ __device__ __forceinline__ void place(const GemmArgs &p, int &tm, int &tn, int &
 // Position of 16-byte chunk c of a row in LDS: c ^ perm.  The sixteen rows that a fragment read
 // covers (consecutive ones of a; of b as col_in_wave has them) then fall on all 64 banks.
 __device__ constexpr int perm(int row) { return (row >> 1) & 7; }
-template <bool WIDE>
+template <bool F32>
 __device__ constexpr int perm_b(int row)
 {
-    return WIDE ? perm(row) : (((row >> 3) & 3) << 1) | ((row >> 1) & 1);
+    return F32 ? perm(row) : (((row >> 3) & 3) << 1) | ((row >> 1) & 1);
 }
-// Which of the wave's columns result e of lane group g in product i is.  16-bit outputs: the
+// Which of the wave's columns result e of lane group g in product i is (F32: of float outputs,
+// four consecutive columns a store).  16-bit outputs: the
 // two products of a pair make eight consecutive columns, one 16-byte store, and the four lane
 // groups of a row 64 bytes.  (Quads of 8 bytes, 32 bytes a row, made stores the bound:
 // 200704 x 128 x 512 took 92 us, 33 without its stores.)
-template <bool WIDE>
+template <bool F32>
 __device__ constexpr int col_in_wave(int i, int g, int e)
 {
-    return WIDE ? 16 * i + 4 * g + e : 32 * (i >> 1) + 8 * g + 4 * (i & 1) + e;
+    return F32 ? 16 * i + 4 * g + e : 32 * (i >> 1) + 8 * g + 4 * (i & 1) + e;
 }
 
 // Tile kernel: 16 MS WM x 16 NS WN results a workgroup, WM x WN waves of 16 MS x 16 NS.
 // Both operands' rows of a k block (128 bytes) and their scales come straight into LDS, NST
 // blocks deep: while block t is multiplied, blocks t + 1 .. t + NST - 1 are on their way, and
 // a wave waits for its own loads of a block by their count, then for the other waves at the
-// one barrier a block.  WIDE: through bf16.
+// one barrier a block.  WIDE: through bf16.  F32: float outputs.
 // 8192^3, bf16 out (256 x 256 tiles): 454 to 484 us = 2.3 to 2.4 PF; bound by the matrix and
 // vector units taking turns (a block's results are scaled and added by the vector unit: 64
 // instructions to 32 products a wave) and by the barrier of two blocks.
 template <int BM, int BN>
 constexpr int stage_bytes() { return (BM + BN) * BK + (BM + BN) * 4; }   // rows, then scales
 
-template <int MS, int NS, int WM, int WN, int NST, int FA, int FB, int BB, bool WIDE>
+template <int MS, int NS, int WM, int WN, int NST, int FA, int FB, int BB, bool WIDE, bool F32>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
 {
     constexpr int NW = WM * WN, BM = 16 * MS * WM, BN = 16 * NS * WN;
@@ -287,6 +290,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
     static_assert(32 * NW % BM == 0 && 32 * NW % BN == 0, "half the waves load the scales of a, half those of b");
     static_assert(BB == 1 || 128 % (16 * NS) == 0, "a wave's columns lie in one block of b");
     static_assert(NS % 2 == 0, "products in pairs");
+    static_assert(WIDE || !F32, "float outputs have fp32 sums");
     static_assert(MS >= 2, "the next block's loads are issued at the second fragment");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const uint32_t lbase = (uint32_t)(uintptr_t)(lds_u8 *)lds;
@@ -308,7 +312,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
     const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void *)(p.b + (int64_t)n0 * p.ldb), 0,
                                                                         (int)((uint32_t)rows_b * p.ldb), 0x00020000);
     const int lrow = 8 * wave + (lane >> 3);
-    const int lchunk = 16 * ((lane & 7) ^ perm(lrow)), lchunk_b = 16 * ((lane & 7) ^ perm_b<WIDE>(lrow));
+    const int lchunk = 16 * ((lane & 7) ^ perm(lrow)), lchunk_b = 16 * ((lane & 7) ^ perm_b<F32>(lrow));
     // 64 scales a wave: of a the first half of the waves, of b the others
     const bool a_scales = wave < NW / 2;
     const int s_at = a_scales ? wave * 64 % BM : (wave - NW / 2) * 64 % BN;
@@ -337,10 +341,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         for (int j = 0; j < MS; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     const uint32_t fa0 = lbase + (wm * 16 * MS + r16) * BK + 16 * (g ^ perm(r16));
-    const int brow = col_in_wave<WIDE>(0, r16 >> 2, r16 & 3);
-    const uint32_t fb0 = lbase + (BM + wn * 16 * NS + brow) * BK + 16 * (g ^ perm_b<WIDE>(brow));
+    const int brow = col_in_wave<F32>(0, r16 >> 2, r16 & 3);
+    const uint32_t fb0 = lbase + (BM + wn * 16 * NS + brow) * BK + 16 * (g ^ perm_b<F32>(brow));
     const uint32_t sa0 = lbase + SCALES + (wm * 16 * MS + r16) * 4;
-    const uint32_t sb0 = lbase + SCALES + BM * 4 + (BB == 1 ? wn * 16 * NS + col_in_wave<WIDE>(0, g, 0) : wn * 16 * NS / 128) * 4;
+    const uint32_t sb0 = lbase + SCALES + BM * 4 + (BB == 1 ? wn * 16 * NS + col_in_wave<F32>(0, g, 0) : wn * 16 * NS / 128) * 4;
 
     const int turns = kb1 - kb0;
 #pragma unroll
@@ -357,7 +361,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
             // the chunk that K ends in: clear what lies past it
             const int kl = p.K - kb * BK, c = kl >> 4, cut = kl & 15;
             for (int r = threadIdx.x; r < BM + BN; r += 64 * NW) {
-                u32x4 *q = (u32x4 *)(lds + st * STAGE + r * BK + 16 * (c ^ (r < BM ? perm(r) : perm_b<WIDE>(r - BM))));
+                u32x4 *q = (u32x4 *)(lds + st * STAGE + r * BK + 16 * (c ^ (r < BM ? perm(r) : perm_b<F32>(r - BM))));
                 u32x4 v = *q;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -379,15 +383,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         if constexpr (BB == 1)
             unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
                 constexpr int i = decltype(ic)::value;
-                t4[i] = __builtin_bit_cast(f32x4, lds_read16<col_in_wave<WIDE>(i, 0, 0) * 4>(sb0 + st * STAGE));
+                t4[i] = __builtin_bit_cast(f32x4, lds_read16<col_in_wave<F32>(i, 0, 0) * 4>(sb0 + st * STAGE));
             });
         else
             s1 = lds_read4<0>(sb0 + st * STAGE);
         u32x4 bf[NS][2], af[3][2];
         unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
             constexpr int i = decltype(ic)::value;
-            bf[i][0] = lds_read16<col_in_wave<WIDE>(i, 0, 0) * BK>(fb);
-            bf[i][1] = lds_read16<col_in_wave<WIDE>(i, 0, 0) * BK>(fbx);
+            bf[i][0] = lds_read16<col_in_wave<F32>(i, 0, 0) * BK>(fb);
+            bf[i][1] = lds_read16<col_in_wave<F32>(i, 0, 0) * BK>(fbx);
         });
         af[0][0] = lds_read16<0>(fa);
         af[0][1] = lds_read16<0>(fax);
@@ -499,7 +503,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
     }
     // Epilogue: bias (0 without one) and activation (a lower bound: 0, or none), then whole
     // chunks, or value by value in the one that N ends in.
-    const int nl = n0 + wn * 16 * NS + col_in_wave<WIDE>(0, g, 0);
+    const int nl = n0 + wn * 16 * NS + col_in_wave<F32>(0, g, 0);
     const int64_t mw = m0 + wm * 16 * MS + r16;
     const bool half = p.d_type == CBR_F16;
     const float *bias = p.part ? nullptr : p.bias;
@@ -507,7 +511,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
     f32x4 bv[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        const int n = nl + col_in_wave<WIDE>(i, 0, 0);
+        const int n = nl + col_in_wave<F32>(i, 0, 0);
         bv[i] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (bias) {
             if (n + 4 <= p.N) bv[i] = *(const f32x4 *)(bias + n);
@@ -524,14 +528,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         return v;
     };
     const int64_t step = 16 * (int64_t)p.N;
-    if (WIDE || p.part) {   // fp32
+    if (F32 || p.part) {
         float *o = (p.part ? p.part + (int64_t)split * p.M * p.N : (float *)p.d) + mw * p.N + nl;
 #pragma unroll
         for (int j = 0; j < MS; ++j, o += step)
             if (mw + 16 * j < p.M)
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
-                    const int c = col_in_wave<WIDE>(i, 0, 0);
+                    const int c = col_in_wave<F32>(i, 0, 0);
                     const f32x4 v = value(i, j);
                     if (nl + c + 4 <= p.N) ((LooseF4 *)(o + c))->v = v;
                     else if (nl + c < p.N)
@@ -546,7 +550,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
             if (mw + 16 * j < p.M)
 #pragma unroll
                 for (int i = 0; i < NS; i += 2) {
-                    const int c = col_in_wave<WIDE>(i, 0, 0);
+                    const int c = col_in_wave<F32>(i, 0, 0);
                     const f32x4 v = value(i, j), w = value(i + 1, j);
                     const u32x4 r = half ? u32x4{F16::pack(v[0], v[1]), F16::pack(v[2], v[3]), F16::pack(w[0], w[1]), F16::pack(w[2], w[3])}
                                          : u32x4{Bf16::pack(v[0], v[1]), Bf16::pack(v[2], v[3]), Bf16::pack(w[0], w[1]), Bf16::pack(w[2], w[3])};
@@ -740,12 +744,12 @@ GemmPlan plan_of(const cbr_gemm_shape &s)
         // (8192 x 8192: 13.1 us for 1 row, 17.8 for 16, 24.7 for 32, 40.2 for 64; tiles take 23)
         least = 2. + (double)s.n * s.k / 6.1e6 * (1. + 0.032 * s.m) + (best.splits > 1 ? 3. : 0.);
     }
-    const bool rows = s.b_block == 1;
+    const bool rows = s.b_block == 1, wide = !s.short_sums;   // (short sums: 16-bit outputs only)
     for (const Form form : {TILE64, TILE128, TILE256}) {
-        if (form == TILE256 && s.d_type == CBR_F32) continue;
+        if (form == TILE256 && wide) continue;   // its widened fragments do not fit the registers
         const Costs c = form == TILE256  ? (rows ? Costs{2.15, 0., 6.} : Costs{1.76, 0., 6.})
-                        : form == TILE64 ? (s.d_type == CBR_F32 ? Costs{0.67, 0.9, 2.} : Costs{0.43, 0.52, 1.6})
-                        : s.d_type == CBR_F32 ? (rows ? Costs{1.15, 2.15, 3.} : Costs{1.0, 1.9, 3.})
+                        : form == TILE64 ? (wide ? Costs{0.67, 0.9, 2.} : Costs{0.43, 0.52, 1.6})
+                        : wide ? (rows ? Costs{1.15, 2.15, 3.} : Costs{1.0, 1.9, 3.})
                                               : (rows ? Costs{0.8, 1.25, 3.} : Costs{0.68, 1.1, 3.});
         const int64_t edge = form == TILE256 ? 256 : form == TILE128 ? 128 : 64, tiles = up(s.m, edge) * up(s.n, edge);
         const int64_t fit = form == TILE256 ? 256 : 512, most = tiles < fit ? std::min(fit / tiles, kbs) : 1;
@@ -766,10 +770,10 @@ GemmPlan plan_of(const cbr_gemm_shape &s)
     return best;
 }
 
-template <int MS, int NS, int WM, int WN, int NST, int FA, int FB, int BB, bool WIDE>
+template <int MS, int NS, int WM, int WN, int NST, int FA, int FB, int BB, bool WIDE, bool F32>
 hipError_t launch_tile(const GemmArgs &a, hipStream_t st)
 {
-    auto k = gemm_tile_kernel<MS, NS, WM, WN, NST, FA, FB, BB, WIDE>;
+    auto k = gemm_tile_kernel<MS, NS, WM, WN, NST, FA, FB, BB, WIDE, F32>;
     constexpr int lds = NST * stage_bytes<16 * MS * WM, 16 * NS * WN>();
     static_assert(lds <= 160 * 1024, "LDS of a CU");
     const hipError_t e = raise_lds_limit((const void *)k, lds);
@@ -777,25 +781,32 @@ hipError_t launch_tile(const GemmArgs &a, hipStream_t st)
     return launch(k, dim3((uint32_t)a.tiles_m * a.tiles_n * a.splits), dim3(64 * WM * WN), lds, st, nullptr, nullptr, a);
 }
 
+template <int FA, int FB, int BB, bool F32>
+hipError_t launch_wide(const GemmPlan &pl, bool deep, const GemmArgs &a, hipStream_t st)
+{
+    if (pl.form == TILE64) return launch_tile<2, 2, 2, 2, 4, FA, FB, BB, true, F32>(a, st);
+    return deep ? launch_tile<4, 2, 2, 4, 4, FA, FB, BB, true, F32>(a, st)
+                : launch_tile<4, 4, 2, 2, 2, FA, FB, BB, true, F32>(a, st);
+}
+
 template <int FA, int FB, int BB>
-hipError_t launch_formats(const GemmPlan &pl, const GemmArgs &a, hipStream_t st)
+hipError_t launch_formats(const GemmPlan &pl, bool short_sums, const GemmArgs &a, hipStream_t st)
 {
     if (pl.form == FEW) {
         auto k = pl.ms == 1 ? gemm_few_kernel<1, FA, FB, BB>
                  : pl.ms == 2 ? gemm_few_kernel<2, FA, FB, BB> : gemm_few_kernel<4, FA, FB, BB>;
         return launch(k, dim3(a.tiles_n, pl.splits), dim3(64 * SKW), 0, st, nullptr, nullptr, a);
     }
-    if (pl.form == TILE256) return launch_tile<8, 4, 2, 4, 2, FA, FB, BB, false>(a, st);
-    if (pl.form == TILE64)
-        return a.d_type == CBR_F32 ? launch_tile<2, 2, 2, 2, 4, FA, FB, BB, true>(a, st)
-                                   : launch_tile<2, 2, 2, 2, 4, FA, FB, BB, false>(a, st);
     // one workgroup a CU: four blocks deep; more: two, and two workgroups share a CU
     const bool deep = (int64_t)a.tiles_m * a.tiles_n * pl.splits <= 256;
-    if (a.d_type == CBR_F32)
-        return deep ? launch_tile<4, 2, 2, 4, 4, FA, FB, BB, true>(a, st)
-                    : launch_tile<4, 4, 2, 2, 2, FA, FB, BB, true>(a, st);
-    return deep ? launch_tile<4, 2, 2, 4, 4, FA, FB, BB, false>(a, st)
-                : launch_tile<4, 2, 2, 4, 2, FA, FB, BB, false>(a, st);
+    if (short_sums) {
+        if (pl.form == TILE256) return launch_tile<8, 4, 2, 4, 2, FA, FB, BB, false, false>(a, st);
+        if (pl.form == TILE64) return launch_tile<2, 2, 2, 2, 4, FA, FB, BB, false, false>(a, st);
+        return deep ? launch_tile<4, 2, 2, 4, 4, FA, FB, BB, false, false>(a, st)
+                    : launch_tile<4, 2, 2, 4, 2, FA, FB, BB, false, false>(a, st);
+    }
+    if (a.d_type == CBR_F32) return launch_wide<FA, FB, BB, true>(pl, deep, a, st);
+    return launch_wide<FA, FB, BB, false>(pl, deep, a, st);
 }
 
 }  // namespace
@@ -834,11 +845,11 @@ hipError_t launch_gemm_fp8(const cbr_gemm_shape &s, const void *a, const float *
     const bool a5 = s.a_type == CBR_E5M2, b5 = s.b_type == CBR_E5M2;
     hipError_t e;
     if (s.b_block == 128)
-        e = a5 ? (b5 ? launch_formats<1, 1, 128>(pl, p, st) : launch_formats<1, 0, 128>(pl, p, st))
-               : (b5 ? launch_formats<0, 1, 128>(pl, p, st) : launch_formats<0, 0, 128>(pl, p, st));
+        e = a5 ? (b5 ? launch_formats<1, 1, 128>(pl, s.short_sums != 0, p, st) : launch_formats<1, 0, 128>(pl, s.short_sums != 0, p, st))
+               : (b5 ? launch_formats<0, 1, 128>(pl, s.short_sums != 0, p, st) : launch_formats<0, 0, 128>(pl, s.short_sums != 0, p, st));
     else
-        e = a5 ? (b5 ? launch_formats<1, 1, 1>(pl, p, st) : launch_formats<1, 0, 1>(pl, p, st))
-               : (b5 ? launch_formats<0, 1, 1>(pl, p, st) : launch_formats<0, 0, 1>(pl, p, st));
+        e = a5 ? (b5 ? launch_formats<1, 1, 1>(pl, s.short_sums != 0, p, st) : launch_formats<1, 0, 1>(pl, s.short_sums != 0, p, st))
+               : (b5 ? launch_formats<0, 1, 1>(pl, s.short_sums != 0, p, st) : launch_formats<0, 0, 1>(pl, s.short_sums != 0, p, st));
     if (e != hipSuccess || pl.splits == 1) return e;
     const int64_t quads = s.m * ((s.n + 3) / 4);
     return launch(gemm_join_kernel, dim3((uint32_t)((quads + 255) / 256)), dim3(256), 0, st, nullptr, nullptr, p, pl.splits);

@@ -106,6 +106,23 @@ __device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi)
     return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// A sum's two scales as factors x, then y.  A sum q is 0 or within 2^-32 .. 2^39, and q sa sb may
+// lie within fp32 where sa sb, or q times one of them, does not.  Scales on the same side of 1 go
+// one after the other (each step lies between q and the result), scales on both sides as their
+// product (which lies between them).
+struct Factors {
+    float x, y;
+    __device__ __forceinline__ Factors(float sa, float sb)
+    {
+        const bool same = (fabsf(sa) > 1.f) == (fabsf(sb) > 1.f);
+        x = same ? sb : sa * sb;
+        y = same ? sa : 1.f;
+    }
+};
+// Whether a sum may always be scaled by s first, whatever the other scale is: s is within 2^-61 ..
+// 2^60, or 0 (or no number at all).
+__device__ __forceinline__ bool mild(float s) { return (uint32_t)(__builtin_amdgcn_frexp_expf(s) + 60) <= 120u; }
+
 // f(integral_constant 0), ... f(integral_constant N - 1)
 template <int N, int I = 0, typename F>
 __device__ __forceinline__ void unrolled(F &&f)
@@ -344,7 +361,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
     const int brow = col_in_wave<F32>(0, r16 >> 2, r16 & 3);
     const uint32_t fb0 = lbase + (BM + wn * 16 * NS + brow) * BK + 16 * (g ^ perm_b<F32>(brow));
     const uint32_t sa0 = lbase + SCALES + (wm * 16 * MS + r16) * 4;
-    const uint32_t sb0 = lbase + SCALES + BM * 4 + (BB == 1 ? wn * 16 * NS + col_in_wave<F32>(0, g, 0) : wn * 16 * NS / 128) * 4;
+    const uint32_t sb0 = lbase + SCALES + (BM + wn * 16 * NS + col_in_wave<F32>(0, g, 0)) * 4;   // (BB 1)
+    const uint32_t look_a = lbase + SCALES + (wm * 16 * MS + lane % (16 * MS)) * 4;
+    const uint32_t look_b = lbase + SCALES + (BM + (BB == 1 ? wn * 16 * NS + lane % (16 * NS) : wn * 16 * NS / 128)) * 4;
 
     const int turns = kb1 - kb0;
 #pragma unroll
@@ -374,45 +393,39 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         }
         const uint32_t fa = fa0 + st * STAGE, fb = fb0 + st * STAGE;
         const uint32_t fax = fa ^ 64, fbx = fb ^ 64;
-        float s[MS], s1;
+        float s[MS], s1, look[2] = {};
         f32x4 t4[BB == 1 ? NS : 1];
-        unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
-            constexpr int j = decltype(jc)::value;
-            s[j] = lds_read4<j * 64>(sa0 + st * STAGE);
-        });
-        if constexpr (BB == 1)
+        // The scales of the wave's columns (BB 128: the one), and for BB 128 those of its rows, 64 a
+        // read, to see which are mild
+        s1 = lds_read4<0>(look_b + st * STAGE);
+        if constexpr (BB != 1) {
+            look[0] = lds_read4<0>(look_a + st * STAGE);
+            if constexpr (MS > 4) look[1] = lds_read4<256>(look_a + st * STAGE);
+        }
+        u32x4 bf[NS][2], af[3][2];
+        auto read = [&]() __attribute__((always_inline)) {
+            unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int j = decltype(jc)::value;
+                s[j] = lds_read4<j * 64>(sa0 + st * STAGE);
+            });
+            if constexpr (BB == 1)
+                unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
+                    constexpr int i = decltype(ic)::value;
+                    t4[i] = __builtin_bit_cast(f32x4, lds_read16<col_in_wave<F32>(i, 0, 0) * 4>(sb0 + st * STAGE));
+                });
             unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
                 constexpr int i = decltype(ic)::value;
-                t4[i] = __builtin_bit_cast(f32x4, lds_read16<col_in_wave<F32>(i, 0, 0) * 4>(sb0 + st * STAGE));
+                bf[i][0] = lds_read16<col_in_wave<F32>(i, 0, 0) * BK>(fb);
+                bf[i][1] = lds_read16<col_in_wave<F32>(i, 0, 0) * BK>(fbx);
             });
-        else
-            s1 = lds_read4<0>(sb0 + st * STAGE);
-        u32x4 bf[NS][2], af[3][2];
-        unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
-            constexpr int i = decltype(ic)::value;
-            bf[i][0] = lds_read16<col_in_wave<F32>(i, 0, 0) * BK>(fb);
-            bf[i][1] = lds_read16<col_in_wave<F32>(i, 0, 0) * BK>(fbx);
-        });
-        af[0][0] = lds_read16<0>(fa);
-        af[0][1] = lds_read16<0>(fax);
-        if constexpr (MS > 1) {
-            af[1][0] = lds_read16<16 * BK>(fa);
-            af[1][1] = lds_read16<16 * BK>(fax);
-        }
-        // Block t + NST - 1 takes the place of block t - 1: every wave is past its reads (their
-        // values went into products) when it reaches the barrier.  Issued among the products:
-        // before the block's first reads, the loads held them up by 500 cycles a block (8192^3
-        // 484 us, 456 right behind the first reads, 454 here).
-        auto load_ahead = [&]() __attribute__((always_inline)) {
-            if (t + NST - 1 < turns) load(kb + NST - 1, st == 0 ? NST - 1 : st - 1);
+            unrolled<2>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int j = decltype(jc)::value;
+                af[j][0] = lds_read16<j * 16 * BK>(fa);
+                af[j][1] = lds_read16<j * 16 * BK>(fax);
+            });
         };
-        f32x4 q[WIDE ? 2 : 1][NS];
-        auto add = [&](int i, int j, const f32x4 &v) __attribute__((always_inline)) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[i][j][e] = fmaf(BB == 1 ? v[e] * t4[BB == 1 ? i : 0][e] : v[e], s[j], acc[i][j][e]);
-        };
-        auto ready = [&]() __attribute__((always_inline)) {   // b's fragments and the scales
+        auto wait = [&]() __attribute__((always_inline)) {   // for all of them
+            lgkm_wait<0>();
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
                 after_wait(bf[i][0]);
@@ -420,84 +433,165 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
             }
 #pragma unroll
             for (int j = 0; j < MS; ++j) after_wait(s[j]);
-            if constexpr (BB == 1) {
+            if constexpr (BB == 1)
 #pragma unroll
                 for (int i = 0; i < NS; ++i) after_wait(t4[i]);
-            } else {
-                after_wait(s1);
 #pragma unroll
-                for (int j = 0; j < MS; ++j) s[j] *= s1;
+            for (int j = 0; j < 2; ++j) {
+                after_wait(af[j][0]);
+                after_wait(af[j][1]);
             }
         };
-        if constexpr (WIDE) {
-            // Fragment j + 1 is widened, and the products of j - 1 are scaled and added, between
-            // the products of j: four vector instructions to a matrix instruction of 16 cycles.
-            // (One after the other, both waves of a SIMD did the same at the same time: 43 us
-            // for 1024 x 256 x 50176, the matrix unit busy 31% of it.)
-            Wide<FB> wb[NS];
-            Wide<FA> wa[2];
-            lgkm_wait<(MS > 1 ? 2 : 0)>();
-            ready();
-            after_wait(af[0][0]);
-            after_wait(af[0][1]);
+        read();
+        // Block t + NST - 1 takes the place of block t - 1: every wave is past its reads (their
+        // values went into products) when it reaches the barrier.  Issued among the products:
+        // before the block's first reads, the loads held them up by 500 cycles a block (8192^3
+        // 484 us, 456 right behind the first reads, 454 here).
+        auto load_ahead = [&]() __attribute__((always_inline)) {
+            if (t + NST - 1 < turns) load(kb + NST - 1, st == 0 ? NST - 1 : st - 1);
+        };
+        constexpr int AFTER = MS + (BB == 1 ? NS : 0) + 2 * NS + 4;   // reads after the first ones
+        lgkm_wait<(AFTER < 15 ? AFTER : 15)>();
+        after_wait(s1);
+        after_wait(look[0]);
+        after_wait(look[1]);
+        // Where all are mild, each sum is multiplied by the product of its scales (BB 128: one for four
+        // results); where only those of b are, by b's and then a's (a multiplication a result more:
+        // rows of a with groups of zeros, whose scale is 2^-126).  Else see below.  Looking costs 2 to
+        // 5% of a call (8192^3 901 -> 932 us, 1024 x 256 x 50176 40.4 -> 43.1), 9% of the smallest tiles.
+        uint32_t how = !mild(s1) ? 2 : !mild(look[0]) || !mild(look[1]) ? 1 : 0;
+        how = __builtin_amdgcn_ballot_w64(how > 1) ? 2 : __builtin_amdgcn_ballot_w64(how > 0) ? 1 : 0;
+        __builtin_amdgcn_sched_barrier(0);
+        wait();   // (nothing may be on its way into a register at a branch that does not use it)
+        auto multiply = [&](auto by_product) __attribute__((always_inline)) {
+            constexpr bool BY_PRODUCT = decltype(by_product)::value;
+            if constexpr (BY_PRODUCT)
 #pragma unroll
-            for (int i = 0; i < NS; ++i) wb[i].set(bf[i][0], bf[i][1]);
-            wa[0].set(af[0][0], af[0][1]);
-            unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
-                constexpr int J = decltype(jc)::value;
-                if constexpr (J + 2 < MS) {   // (its registers were widened two turns ago)
-                    af[(J + 2) % 3][0] = lds_read16<(J + 2) * 16 * BK>(fa);
-                    af[(J + 2) % 3][1] = lds_read16<(J + 2) * 16 * BK>(fax);
-                }
-                if constexpr (J == MS / 2) load_ahead();
-                if constexpr (J + 1 < MS) {
-                    lgkm_wait<(J + 2 < MS ? 2 : 0)>();
-                    after_wait(af[(J + 1) % 3][0]);
-                    after_wait(af[(J + 1) % 3][1]);
-                }
-                __builtin_amdgcn_sched_barrier(0);
+                for (int j = 0; j < MS; ++j) s[j] *= s1;
+            f32x4 q[WIDE ? 2 : 1][NS];
+            auto add = [&](int i, int j, const f32x4 &v) __attribute__((always_inline)) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] = fmaf(BY_PRODUCT ? v[e] : v[e] * (BB == 1 ? t4[BB == 1 ? i : 0][e] : s1), s[j], acc[i][j][e]);
+            };
+            if constexpr (WIDE) {
+                // Fragment j + 1 is widened, and the products of j - 1 are scaled and added, between
+                // the products of j: four vector instructions to a matrix instruction of 16 cycles.
+                // (One after the other, both waves of a SIMD did the same at the same time: 43 us
+                // for 1024 x 256 x 50176, the matrix unit busy 31% of it.)
+                Wide<FB> wb[NS];
+                Wide<FA> wa[2];
 #pragma unroll
-                    for (int i = 0; i < NS; ++i)
-                        q[J % 2][i] = product(wb[i].t[t], wa[J % 2].t[t], t == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : q[J % 2][i]);
-                if constexpr (J + 1 < MS) wa[(J + 1) % 2].set(af[(J + 1) % 3][0], af[(J + 1) % 3][1]);
-                if constexpr (J > 0)
-#pragma unroll
-                    for (int i = 0; i < NS; ++i) add(i, J - 1, q[(J - 1) % 2][i]);
-#pragma unroll
-                for (int u = 0; u < 4 * NS; ++u) {
-                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);   // a matrix instruction
-                    __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);   // four of the vector unit
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            });
-#pragma unroll
-            for (int i = 0; i < NS; ++i) add(i, MS - 1, q[(MS - 1) % 2][i]);
-        } else {
-            unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
-                constexpr int J = decltype(jc)::value;
-                lgkm_wait<(J + 1 < MS ? 2 : 0)>();   // all but the next fragment of a
-                if constexpr (J == 0) ready();
-                after_wait(af[J % 3][0]);
-                after_wait(af[J % 3][1]);
-                const i32x8 av = join(af[J % 3][0], af[J % 3][1]);
-                if constexpr (J == 1) load_ahead();
-#pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    if constexpr (J > 0) add(i, J - 1, q[0][i]);
-                    q[0][i] = product<FB, FA>(join(bf[i][0], bf[i][1]), av);
-                    // the next fragment but one, once the products that read its registers are under way
-                    if constexpr (J + 2 < MS)
-                        if (i == 0) {
-                            af[(J + 2) % 3][0] = lds_read16<(J + 2) * 16 * BK>(fa);
-                            af[(J + 2) % 3][1] = lds_read16<(J + 2) * 16 * BK>(fax);
-                        }
+                for (int i = 0; i < NS; ++i) wb[i].set(bf[i][0], bf[i][1]);
+                wa[0].set(af[0][0], af[0][1]);
+                unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
+                    constexpr int J = decltype(jc)::value;
+                    if constexpr (J + 2 < MS) {   // (its registers were widened two turns ago)
+                        af[(J + 2) % 3][0] = lds_read16<(J + 2) * 16 * BK>(fa);
+                        af[(J + 2) % 3][1] = lds_read16<(J + 2) * 16 * BK>(fax);
+                    }
+                    if constexpr (J == MS / 2) load_ahead();
+                    if constexpr (J + 1 < MS) {
+                        lgkm_wait<(J + 2 < MS ? 2 : 0)>();
+                        after_wait(af[(J + 1) % 3][0]);
+                        after_wait(af[(J + 1) % 3][1]);
+                    }
                     __builtin_amdgcn_sched_barrier(0);
-                }
-            });
 #pragma unroll
-            for (int i = 0; i < NS; ++i) add(i, MS - 1, q[0][i]);
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int i = 0; i < NS; ++i)
+                            q[J % 2][i] = product(wb[i].t[t], wa[J % 2].t[t], t == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : q[J % 2][i]);
+                    if constexpr (J + 1 < MS) wa[(J + 1) % 2].set(af[(J + 1) % 3][0], af[(J + 1) % 3][1]);
+                    if constexpr (J > 0)
+#pragma unroll
+                        for (int i = 0; i < NS; ++i) add(i, J - 1, q[(J - 1) % 2][i]);
+#pragma unroll
+                    for (int u = 0; u < 4 * NS; ++u) {
+                        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);   // a matrix instruction
+                        __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);   // four of the vector unit
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+#pragma unroll
+                for (int i = 0; i < NS; ++i) add(i, MS - 1, q[(MS - 1) % 2][i]);
+            } else {
+                unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
+                    constexpr int J = decltype(jc)::value;
+                    lgkm_wait<(J + 1 < MS ? 2 : 0)>();   // all but the next fragment of a
+                    after_wait(af[J % 3][0]);
+                    after_wait(af[J % 3][1]);
+                    const i32x8 av = join(af[J % 3][0], af[J % 3][1]);
+                    if constexpr (J == 1) load_ahead();
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) {
+                        if constexpr (J > 0) add(i, J - 1, q[0][i]);
+                        q[0][i] = product<FB, FA>(join(bf[i][0], bf[i][1]), av);
+                        // the next fragment but one, once the products that read its registers are under way
+                        if constexpr (J + 2 < MS)
+                            if (i == 0) {
+                                af[(J + 2) % 3][0] = lds_read16<(J + 2) * 16 * BK>(fa);
+                                af[(J + 2) % 3][1] = lds_read16<(J + 2) * 16 * BK>(fax);
+                            }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                });
+#pragma unroll
+                for (int i = 0; i < NS; ++i) add(i, MS - 1, q[0][i]);
+            }
+        };
+        // One `if` after another: as two sides of a branch the sums do not stay in place (120 registers spilled).
+        if (__builtin_expect(how == 0, 1)) multiply(std::integral_constant<bool, BB != 1>{});
+        after_wait(how);
+        if constexpr (BB != 1) {
+            if (__builtin_expect(__builtin_amdgcn_readfirstlane(how) == 1, 0)) {
+                read();
+                wait();
+                multiply(std::false_type{});
+            }
+            after_wait(how);
+        }
+        // Scales of b that are not mild (groups of zeros there, say): product by product, everything read
+        // again, in the order that Factors takes.  Twice the time for such a block.
+        if (__builtin_expect(__builtin_amdgcn_readfirstlane(how) == 2, 0)) {
+            load_ahead();
+            unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
+                constexpr int J = decltype(jc)::value;
+                u32x4 a0 = lds_read16<J * 16 * BK>(fa), a1 = lds_read16<J * 16 * BK>(fax);
+                float sa = lds_read4<J * 64>(sa0 + st * STAGE);
+                unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
+                    constexpr int I = decltype(ic)::value;
+                    u32x4 b0 = lds_read16<col_in_wave<F32>(I, 0, 0) * BK>(fb), b1 = lds_read16<col_in_wave<F32>(I, 0, 0) * BK>(fbx);
+                    f32x4 sb;
+                    if constexpr (BB == 1)
+                        sb = __builtin_bit_cast(f32x4, lds_read16<col_in_wave<F32>(I, 0, 0) * 4>(sb0 + st * STAGE));
+                    else
+                        sb[0] = s1;
+                    lgkm_wait<0>();
+                    after_wait(a0);
+                    after_wait(a1);
+                    after_wait(sa);
+                    after_wait(b0);
+                    after_wait(b1);
+                    after_wait(sb);
+                    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+                    if constexpr (WIDE) {
+                        Wide<FA> wa;
+                        Wide<FB> wb;
+                        wa.set(a0, a1);
+                        wb.set(b0, b1);
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) v = product(wb.t[t], wa.t[t], v);
+                    } else {
+                        v = product<FB, FA>(join(b0, b1), join(a0, a1));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const Factors f(sa, sb[BB == 1 ? e : 0]);
+                        acc[I][J][e] = fmaf(v[e] * f.x, f.y, acc[I][J][e]);
+                    }
+                });
+            });
         }
         st = st + 1 == NST ? 0 : st + 1;
     }
@@ -618,7 +712,10 @@ __global__ __launch_bounds__(64 * SKW) void gemm_few_kernel(GemmArgs p)
 #pragma unroll
             for (int t = 0; t < 4; ++t) q = product(wb.t[t], wa.t[t], q);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(q[e] * o.sb[BB == 1 ? e : 0], o.sa[j], acc[j][e]);
+            for (int e = 0; e < 4; ++e) {
+                const Factors f(o.sa[j], o.sb[BB == 1 ? e : 0]);
+                acc[j][e] = fmaf(q[e] * f.x, f.y, acc[j][e]);
+            }
         }
     };
     const int full = min(kb1, p.K / BK);   // blocks that K does not end in

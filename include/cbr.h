@@ -324,7 +324,9 @@ int cbr_fp8_quantize(const cbr_quant_shape *shape, const void *src, void *q, flo
  * multiples of 16 and at least k; what lies past k in a row is not used.  a_scale
  * [ceil(k/128)][m] (block 1), b_scale [ceil(k/128)][ceil(n / b_block)], b_block 1 or 128.
  * d [m][n] dense, d_type CBR_BF16, CBR_F16 or CBR_F32; bias float [n] or NULL; act is
- * max(v, 0) where relu is non-zero (a NaN stays one), else v.  All sums are fp32, and the
+ * max(v, 0) where relu is non-zero (a NaN stays one), else v.  Scales may have any size: a
+ * sum is not lost where a_scale * b_scale, or the sum times one of them, leaves fp32 and the
+ * result does not (scales of b outside 2^-61 .. 2^60 cost time).  All sums are fp32, and the
  * result is rounded once, unless short_sums is non-zero: then each eight consecutive products
  * (k = 8i .. 8i + 7) may be summed with 13 bits below the leading one of the largest, by the
  * 8-bit matrix instruction at twice the rate, and everything beyond the eight in fp32.  An

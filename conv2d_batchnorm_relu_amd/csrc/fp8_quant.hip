@@ -3,10 +3,15 @@
 //
 //   a = max(largest |v|, fmax 2^-126),  scale = a / fmax,  q = rne(v fmax / a)
 // The quotient is the correctly rounded one: with a = m 2^e (m in [1/2, 1)), n = v (fmax 2^-e)
-// (exact for 16-bit sources: fmax is 7 times a power of two), q0 = n (1/m), and one step of
-// Markstein's division, q0 + (n - q0 m)(1/m).  A value midway between two 8-bit ones (3/4 of
-// a power of two times the largest, say) is then met exactly and goes to the even one; a
-// product with a rounded reciprocal sends a part of them astray.
+// (fmax is 7 times a power of two: exact for 16-bit sources; of an fp32 one the error is carried
+// along), q0 = n (1/m), and one step of Markstein's division, q0 + (n - q0 m)(1/m).  A value midway
+// between two 8-bit ones (3/4 of a power of two times the largest, say) is then met exactly and goes
+// to the even one; a product with a rounded reciprocal sends a part of them astray.  Quotients of
+// 16-bit values that are not midway are 2^-16 of their size off, so fp32 tells them apart; those of
+// fp32 values may be 2^-28 off.  There the quotient is rounded to odd: an inexact one has its last
+// bit set (one step towards the exact value where it was not), and the rounding to 8 bits goes the
+// way that the exact value says.  That is three times the arithmetic, so it is done only where n (1/m)
+// moved by 2^-21 of itself up and down rounds to two values: 1 of 2^16 where mantissas are random.
 // Bound by memory: 2 or 4 bytes read and 1 written for each value (50176 x 1024 bf16 turned
 // over: 28 us = 5.5 TB/s; 64 x 2048: 2.8 us).
 #include "block_launch.h"
@@ -16,7 +21,7 @@ namespace cbr {
 namespace {
 
 // What turns a group's values into 8 bits: t = v fmax / a (Markstein's correction), then rounding.
-template <bool E5M2>
+template <typename T, bool E5M2>
 struct Group {
     float c, m, rm, scale;
 
@@ -35,10 +40,20 @@ struct Group {
             m = rm = 1.f;
         }
     }
-    __device__ __forceinline__ float operator()(float v) const
+    __device__ __forceinline__ float near(float v) const { return v * c * rm; }   // within 2^-22 of itself
+    __device__ __forceinline__ float exact(float v) const
     {
         const float n = v * c, q0 = n * rm;
-        return fmaf(fmaf(-q0, m, n), rm, q0);
+        if constexpr (T::SIZE == 2) {
+            return fmaf(fmaf(-q0, m, n), rm, q0);
+        } else {
+            const float lo = fmaf(v, c, -n);                                 // n + lo = v c
+            const float t = fmaf(fmaf(-q0, m, n) + lo, rm, q0);
+            const float r = fmaf(-t, m, n) + lo;                             // (v c / m - t) m
+            const int b = __float_as_int(t);
+            const bool odd = (b & 1) || !(fabsf(r) > 0.f);                   // odd, exact or NaN: as it is
+            return odd ? t : __int_as_float(b + ((b ^ __float_as_int(r)) < 0 ? -1 : 1));
+        }
     }
 };
 
@@ -55,6 +70,19 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d)
         r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
     }
     return (uint32_t)r;
+}
+
+// Four values of a group.
+template <typename T, bool E5M2>
+__device__ __forceinline__ uint32_t encode4(const Group<T, E5M2> &g, float a, float b, float c, float d)
+{
+    if constexpr (T::SIZE == 4) {
+        constexpr float UP = 1.f + 0x1p-21f, DOWN = 1.f - 0x1p-21f;
+        const float na = g.near(a), nb = g.near(b), nc = g.near(c), nd = g.near(d);
+        const uint32_t up = pack4<E5M2>(na * UP, nb * UP, nc * UP, nd * UP);
+        if (__builtin_expect(up == pack4<E5M2>(na * DOWN, nb * DOWN, nc * DOWN, nd * DOWN), 1)) return up;
+    }
+    return pack4<E5M2>(g.exact(a), g.exact(b), g.exact(c), g.exact(d));
 }
 
 // Eight values of a row at column col, zeros past its end.  The last, partial chunk of a row
@@ -102,11 +130,9 @@ __global__ __launch_bounds__(NT) void quant_rows_kernel(const char *__restrict__
         for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
 #pragma unroll
         for (int off = 1; off < 16; off <<= 1) amax = fmaxf(amax, __shfl_xor(amax, off));
-        Group<E5M2> g;
+        Group<T, E5M2> g;
         g.set(amax);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = g(v[e]);
-        const uint32_t lo = pack4<E5M2>(v[0], v[1], v[2], v[3]), hi = pack4<E5M2>(v[4], v[5], v[6], v[7]);
+        const uint32_t lo = encode4(g, v[0], v[1], v[2], v[3]), hi = encode4(g, v[4], v[5], v[6], v[7]);
         if (row >= rows) continue;
         if (lane == 0) scale[kb * rows + row] = g.scale;
         uint8_t *p = q + row * ldq + col;
@@ -152,7 +178,7 @@ __global__ __launch_bounds__(NT) void quant_tile_kernel(const char *__restrict__
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax[e] = fmaxf(amax[e], fabsf(v[e]));
     }
-    Group<E5M2> g[BLOCK == 1 ? 8 : 1];
+    Group<T, E5M2> g[BLOCK == 1 ? 8 : 1];
     if constexpr (BLOCK == 1) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -167,7 +193,7 @@ __global__ __launch_bounds__(NT) void quant_tile_kernel(const char *__restrict__
         // took 3 us of the smallest call's 8)
         if (threadIdx.x < TS) {
             const int c = threadIdx.x;
-            Group<E5M2> w;
+            Group<T, E5M2> w;
             w.set(fmaxf(fmaxf(red[0][c], red[1][c]), fmaxf(red[2][c], red[3][c])));
             groups[c] = f32x4{w.c, w.m, w.rm, w.scale};
             if (ct * TS + c < cols) scale[rt * cols + ct * TS + c] = w.scale;
@@ -197,9 +223,7 @@ __global__ __launch_bounds__(NT) void quant_tile_kernel(const char *__restrict__
             if (row0 + i >= rows) break;
             float v[8];
             unpack8<T>(raw[i], v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = g[0](v[e]);
-            const uint32_t lo = pack4<E5M2>(v[0], v[1], v[2], v[3]), hi = pack4<E5M2>(v[4], v[5], v[6], v[7]);
+            const uint32_t lo = encode4(g[0], v[0], v[1], v[2], v[3]), hi = encode4(g[0], v[4], v[5], v[6], v[7]);
             uint8_t *p = q + (row0 + i) * ldq + col;
             if (col + (TAIL ? 8 : 1) <= cols) {
                 *(uint2 *)p = make_uint2(lo, hi);
@@ -214,14 +238,10 @@ __global__ __launch_bounds__(NT) void quant_tile_kernel(const char *__restrict__
         for (int h = 0; h < 2; ++h) {   // four rows make a word of each column
             float v[4][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                unpack8<T>(raw[4 * h + i], v[i]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = g[BLOCK == 1 ? e : 0](v[i][e]);
-            }
+            for (int i = 0; i < 4; ++i) unpack8<T>(raw[4 * h + i], v[i]);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                turn[(cl * 8 + e) * LROW + rl * 2 + h] = pack4<E5M2>(v[0][e], v[1][e], v[2][e], v[3][e]);
+                turn[(cl * 8 + e) * LROW + rl * 2 + h] = encode4(g[BLOCK == 1 ? e : 0], v[0][e], v[1][e], v[2][e], v[3][e]);
         }
         __syncthreads();
         // eight threads a column, 16 bytes each

@@ -14,6 +14,8 @@
 // moved by 2^-21 of itself up and down rounds to two values: 1 of 2^16 where mantissas are random.
 // Bound by memory: 2 or 4 bytes read and 1 written for each value (50176 x 1024 bf16 turned
 // over: 28 us = 5.5 TB/s; 64 x 2048: 2.8 us).
+#include <type_traits>
+
 #include "block_launch.h"
 #include "block_types.h"
 
@@ -85,6 +87,16 @@ __device__ __forceinline__ uint32_t encode4(const Group<T, E5M2> &g, float a, fl
     return pack4<E5M2>(g.exact(a), g.exact(b), g.exact(c), g.exact(d));
 }
 
+// The larger of m and |v|; m where v is a NaN.  The hardware's maximum is one of its operands where
+// the other is a quiet NaN, but a NaN where it is a signalling one: those are made quiet first (f16
+// ones are when they become float).
+template <typename T>
+__device__ __forceinline__ float larger(float m, float v)
+{
+    if constexpr (std::is_same_v<T, F16>) return fmaxf(m, fabsf(v));
+    else return fmaxf(m, __builtin_canonicalizef(fabsf(v)));
+}
+
 // Eight values of a row at column col, zeros past its end.  The last, partial chunk of a row
 // is loaded as the row's last eight values and moved to the front by settle8, once all loads
 // are out: value by value, each would be waited for.
@@ -127,7 +139,7 @@ __global__ __launch_bounds__(NT) void quant_rows_kernel(const char *__restrict__
         settle8<T, TAIL>(col, cols, raw[u]);
         unpack8<T>(raw[u], v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+        for (int e = 0; e < 8; ++e) amax = larger<T>(amax, v[e]);
 #pragma unroll
         for (int off = 1; off < 16; off <<= 1) amax = fmaxf(amax, __shfl_xor(amax, off));
         Group<T, E5M2> g;
@@ -176,7 +188,7 @@ __global__ __launch_bounds__(NT) void quant_tile_kernel(const char *__restrict__
         settle8<T, TAIL>(col, cols, raw[i]);
         unpack8<T>(raw[i], v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax[e] = fmaxf(amax[e], fabsf(v[e]));
+        for (int e = 0; e < 8; ++e) amax[e] = larger<T>(amax[e], v[e]);
     }
     Group<T, E5M2> g[BLOCK == 1 ? 8 : 1];
     if constexpr (BLOCK == 1) {

@@ -194,3 +194,24 @@ def test_short_sums_are_as_near_as_the_header_says(k, kind, stated):
     got = ws[:splits * 4 * m * n].view(torch.float32).view(splits, m, n).double().sum(0)
     want = av @ bv.t()
     assert (got - want).norm() <= 2 * stated * want.norm()
+
+
+@gpu
+@pytest.mark.parametrize("m", [96, 300, 2048])
+def test_short_sums_keep_thirteen_bits(m):
+    """A product of 2^-13 of the largest of its eight survives the largest's cancelling in another eight,
+    in every tile."""
+    n, k = 2048 if m == 2048 else 200, 128
+    av, bv = torch.zeros(m, k, device="cuda"), torch.zeros(n, k, device="cuda")
+    for place in range(1, 8):
+        av.zero_(), bv.zero_()
+        av[:, 8] = bv[:, 8] = 1.0
+        av[:, 8 + place], bv[:, 8 + place] = 2.0 ** -6, 2.0 ** -7
+        av[:, 64], bv[:, 64] = 1.0, -1.0
+        sp = cbr.make_gemm_shape(m, n, k, d_type=cbr.CBR_BF16, short_sums=True)
+        ws = torch.empty(max(16, cbr.cbr_gemm_fp8_workspace_bytes(sp)), dtype=torch.uint8, device="cuda")
+        d = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+        one = lambda r: torch.ones(1, r, device="cuda")  # noqa: E731
+        cbr.cbr_gemm_fp8(sp, raw(av, torch.float8_e4m3fn, k), one(m), raw(bv, torch.float8_e4m3fn, k), one(-(-n // 128)), None,
+                         d, ws)
+        assert (d == 2.0 ** -13).all()

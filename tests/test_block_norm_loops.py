@@ -109,3 +109,19 @@ def test_gradients_of_a_bf16_stream_against_the_forward_as_it_ran():
     assert ((g["dx"].double() - d).abs() <= 2.0 ** -8 * (d.abs() + ed) + ed).all()
     tol = (w["dh"].abs() * e).sum(0) + (700 + 64) * B.U * (w["dh"].abs() * (yh.abs() + e)).sum(0)
     assert ((g["pre_w"].double() - (w["dh"] * yh).sum(0)).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("c", [520, 1001, 2049, 4099, 8191])
+@pytest.mark.parametrize("post,pre", [("none", "none"), ("none", "rms"), ("layer", "none"), ("layer", "layer")])
+def test_in_place_rows_of_several_waves(c, post, pre):
+    """y in x, h in f, dx in dy, df in f, where several waves share a row and (but for 520) its last chunk is a
+    part of one, read as the row's last eight values: other waves may be storing those it drops."""
+    t = B.make(700, c, "bf16", "bf16", post, pre, 7, c)
+    o = B.run_forward(t)
+    x, f = t["x"].clone(), t["f"].clone()
+    o2 = B.run_forward({**t, "x": x, "f": f}, y=x, h=f if pre != "none" else None)
+    assert torch.equal(o2["y"], o["y"]) and (pre == "none" or torch.equal(o2["h"], o["h"]))
+    g = B.run_backward(t, o)
+    dy, f = t["dy"].clone(), t["f"].clone()
+    g2 = B.run_backward({**t, "dy": dy, "f": f}, o, dx=dy, df=f)
+    assert all((g[k] is None and g2[k] is None) or torch.equal(g[k], g2[k]) for k in g)

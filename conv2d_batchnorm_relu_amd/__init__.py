@@ -23,11 +23,16 @@ __all__ = ["CbrError", "CbrShape", "make_shape", "cbr_status_str", "cbr_output_h
            "CbrBlockShape", "make_block_shape", "cbr_block_norm_workspace_bytes", "cbr_block_norm_forward",
            "cbr_block_norm_backward", "CbrQuantShape", "make_quant_shape", "cbr_fp8_quantize", "CbrGemmShape",
            "make_gemm_shape", "cbr_gemm_fp8_workspace_bytes", "cbr_gemm_fp8", "CBR_BF16", "CBR_F16", "CBR_F32",
-           "CBR_E4M3", "CBR_E5M2", "CBR_NORM_NONE", "CBR_NORM_RMS", "CBR_NORM_LAYER"]
+           "CBR_E4M3", "CBR_E5M2", "CBR_NORM_NONE", "CBR_NORM_RMS", "CBR_NORM_LAYER",
+           "CbrGroupNormShape", "make_group_norm_shape", "cbr_group_norm_workspace_bytes", "cbr_group_norm_forward",
+           "cbr_group_norm_backward", "CbrFp4Shape", "make_fp4_shape", "cbr_fp4_quantize", "cbr_fp4_dequantize",
+           "CbrGemmFp4Shape", "make_gemm_fp4_shape", "cbr_gemm_fp4_workspace_bytes", "cbr_gemm_fp4", "CBR_ACT_NONE",
+           "CBR_ACT_RELU", "CBR_ACT_SILU"]
 
 CBR_OP_TRAIN, CBR_OP_INFER, CBR_OP_BWD = 0, 1, 2
 CBR_BF16, CBR_F16, CBR_F32, CBR_E4M3, CBR_E5M2 = 0, 1, 2, 3, 4
 CBR_NORM_NONE, CBR_NORM_RMS, CBR_NORM_LAYER = 0, 1, 2
+CBR_ACT_NONE, CBR_ACT_RELU, CBR_ACT_SILU = 0, 1, 2
 _BYTES = {CBR_BF16: 2, CBR_F16: 2, CBR_F32: 4, CBR_E4M3: 1, CBR_E5M2: 1}
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libcbr.so")
@@ -56,6 +61,21 @@ class CbrGemmShape(ctypes.Structure):
                 ("ldb", ctypes.c_int64), ("a_type", ctypes.c_int32), ("b_type", ctypes.c_int32),
                 ("d_type", ctypes.c_int32), ("b_block", ctypes.c_int32), ("relu", ctypes.c_int32),
                 ("short_sums", ctypes.c_int32)]
+
+
+class CbrGroupNormShape(ctypes.Structure):
+    _fields_ = [("images", ctypes.c_int64), ("pixels", ctypes.c_int64), ("channels", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("type", ctypes.c_int32), ("act", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class CbrFp4Shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ldq", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("transpose", ctypes.c_int32)]
+
+
+class CbrGemmFp4Shape(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("lda", ctypes.c_int64),
+                ("ldb", ctypes.c_int64), ("d_type", ctypes.c_int32), ("relu", ctypes.c_int32)]
 
 
 class CbrError(RuntimeError):
@@ -117,13 +137,21 @@ def _load():
         fe.argtypes = fn.argtypes + [P]
         fe.restype = ctypes.c_int
     B, U, G = (ctypes.POINTER(t) for t in (CbrBlockShape, CbrQuantShape, CbrGemmShape))
+    N, Q, H = (ctypes.POINTER(t) for t in (CbrGroupNormShape, CbrFp4Shape, CbrGemmFp4Shape))
     for name, args, res in (
             ("cbr_block_norm_workspace_bytes", [B], ctypes.c_size_t),
             ("cbr_block_norm_forward", [B] + [P] * 13, ctypes.c_int),
             ("cbr_block_norm_backward", [B] + [P] * 20 + [ctypes.c_size_t, P], ctypes.c_int),
             ("cbr_fp8_quantize", [U] + [P] * 4, ctypes.c_int),
             ("cbr_gemm_fp8_workspace_bytes", [G], ctypes.c_size_t),
-            ("cbr_gemm_fp8", [G] + [P] * 7 + [ctypes.c_size_t, P], ctypes.c_int)):
+            ("cbr_gemm_fp8", [G] + [P] * 7 + [ctypes.c_size_t, P], ctypes.c_int),
+            ("cbr_group_norm_workspace_bytes", [N, ctypes.c_int], ctypes.c_size_t),
+            ("cbr_group_norm_forward", [N] + [P] * 6 + [ctypes.c_size_t, P], ctypes.c_int),
+            ("cbr_group_norm_backward", [N] + [P] * 9 + [ctypes.c_size_t, P], ctypes.c_int),
+            ("cbr_fp4_quantize", [Q] + [P] * 4, ctypes.c_int),
+            ("cbr_fp4_dequantize", [Q] + [P] * 4, ctypes.c_int),
+            ("cbr_gemm_fp4_workspace_bytes", [H], ctypes.c_size_t),
+            ("cbr_gemm_fp4", [H] + [P] * 7 + [ctypes.c_size_t, P], ctypes.c_int)):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = res
     _lib = lib
@@ -312,6 +340,10 @@ def cbr_conv2d_bias(shape, x, w, bias, y, stream=None, events=None):
 _DTYPES = {CBR_BF16: ("bfloat16", "int16", "uint16"), CBR_F16: ("float16", "int16", "uint16"),
            CBR_F32: ("float32",), CBR_E4M3: ("float8_e4m3fn", "uint8", "int8"),
            CBR_E5M2: ("float8_e5m2", "uint8", "int8")}
+# The bytes of 4-bit operands (two values each) and of their scales.
+_FP4, _E8M0 = "fp4", "e8m0"
+_DTYPES.update({_FP4: ("uint8", "int8", "float4_e2m1fn_x2"), _E8M0: ("uint8", "int8", "float8_e8m0fnu")})
+_BYTES.update({_FP4: 1, _E8M0: 1})
 
 
 class _Call:
@@ -464,3 +496,86 @@ def cbr_gemm_fp8(shape, a, a_scale, b, b_scale, bias, d, workspace=None, stream=
                                 at(b_scale, CBR_F32, "b_scale", kb * -(-n // s.b_block)),
                                 at(bias, CBR_F32, "bias", n), at(d, s.d_type, "d", m * n), ws, nbytes,
                                 call.stream(stream)), call.where)
+
+
+def make_group_norm_shape(images, pixels, channels, groups, dtype=CBR_BF16, act=CBR_ACT_NONE, eps=1e-5) -> CbrGroupNormShape:
+    """pixels: H * W of an image."""
+    return CbrGroupNormShape(images, pixels, channels, groups, dtype, act, eps)
+
+
+def cbr_group_norm_workspace_bytes(shape: CbrGroupNormShape, backward=False) -> int:
+    return int(_load().cbr_group_norm_workspace_bytes(_sp(shape), int(bool(backward))))
+
+
+def cbr_group_norm_forward(shape, x, w, b, y, stats=None, workspace=None, stream=None):
+    """y = act(group_norm(x) * w + b) over channels-last maps (include/cbr.h); None is a pointer that is not given."""
+    s = shape
+    call = _Call("cbr_group_norm_forward", s.type)
+    at, c, n = call.at, s.channels, s.images * s.pixels * s.channels
+    ws, nbytes = call.workspace(workspace)
+    _check(_load().cbr_group_norm_forward(_sp(s), at(x, s.type, "x", n), at(w, CBR_F32, "w", c), at(b, CBR_F32, "b", c),
+                                          at(y, s.type, "y", n), at(stats, CBR_F32, "stats", 2 * s.images * s.groups), ws,
+                                          nbytes, call.stream(stream)), call.where)
+
+
+def cbr_group_norm_backward(shape, dy, x, w, b, stats, dx, dw, db, workspace=None, stream=None):
+    """Gradients of cbr_group_norm_forward; None is a pointer that is not given (a gradient that is not wanted)."""
+    s = shape
+    call = _Call("cbr_group_norm_backward", s.type)
+    at, c, n = call.at, s.channels, s.images * s.pixels * s.channels
+    ws, nbytes = call.workspace(workspace)
+    _check(_load().cbr_group_norm_backward(
+        _sp(s), at(dy, s.type, "dy", n), at(x, s.type, "x", n), at(w, CBR_F32, "w", c), at(b, CBR_F32, "b", c),
+        at(stats, CBR_F32, "stats", 2 * s.images * s.groups), at(dx, s.type, "dx", n), at(dw, CBR_F32, "dw", c),
+        at(db, CBR_F32, "db", c), ws, nbytes, call.stream(stream)), call.where)
+
+
+def make_fp4_shape(rows, cols, dtype=CBR_BF16, transpose=False, ldq=None) -> CbrFp4Shape:
+    """ldq None: sixteen bytes for each 32 values of a row of the 4-bit form."""
+    if ldq is None:
+        ldq = -(-(rows if transpose else cols) // 32) * 16
+    return CbrFp4Shape(rows, cols, ldq, dtype, int(bool(transpose)))
+
+
+def _fp4_call(name, shape, of_type, of_type_name, q, scale, stream):
+    s = shape
+    call = _Call(name, s.type)
+    rows, cols = (s.cols, s.rows) if s.transpose else (s.rows, s.cols)
+    v = call.at(of_type, s.type, of_type_name, rows * cols)
+    q = call.at(q, _FP4, "q", (rows - 1) * s.ldq + -(-cols // 32) * 16)
+    e = call.at(scale, _E8M0, "scale", -(-cols // 128) * rows * 4)
+    args = (v, q, e) if of_type_name == "src" else (q, e, v)
+    _check(getattr(_load(), name)(_sp(s), *args, call.stream(stream)), name)
+
+
+def cbr_fp4_quantize(shape, src, q, scale, stream=None):
+    """src (or its transpose) in 4 bits, q [rows][ldq] bytes, with its scales [ceil(cols / 128)][rows][4] (include/cbr.h)."""
+    _fp4_call("cbr_fp4_quantize", shape, src, "src", q, scale, stream)
+
+
+def cbr_fp4_dequantize(shape, q, scale, v, stream=None):
+    """v [rows][cols]: what q and scale, as cbr_fp4_quantize left them for this shape, stand for."""
+    _fp4_call("cbr_fp4_dequantize", shape, v, "v", q, scale, stream)
+
+
+def make_gemm_fp4_shape(m, n, k, d_type=CBR_BF16, relu=False, lda=None, ldb=None) -> CbrGemmFp4Shape:
+    """lda, ldb None: sixteen bytes for each 32 values."""
+    ld = -(-k // 32) * 16
+    return CbrGemmFp4Shape(m, n, k, ld if lda is None else lda, ld if ldb is None else ldb, d_type, int(bool(relu)))
+
+
+def cbr_gemm_fp4_workspace_bytes(shape: CbrGemmFp4Shape) -> int:
+    return int(_load().cbr_gemm_fp4_workspace_bytes(_sp(shape)))
+
+
+def cbr_gemm_fp4(shape, a, a_scale, b, b_scale, bias, d, workspace=None, stream=None):
+    """d = act((a * a_scale) (b * b_scale)^T + bias) of 4-bit operands (include/cbr.h); workspace may be None where
+    cbr_gemm_fp4_workspace_bytes is 0."""
+    s = shape
+    call = _Call("cbr_gemm_fp4", s.d_type)
+    m, n, words, row, at = s.m, s.n, -(-s.k // 128), -(-s.k // 32) * 16, call.at
+    ws, nbytes = call.workspace(workspace)
+    _check(_load().cbr_gemm_fp4(_sp(s), at(a, _FP4, "a", (m - 1) * s.lda + row), at(a_scale, _E8M0, "a_scale", words * m * 4),
+                                at(b, _FP4, "b", (n - 1) * s.ldb + row), at(b_scale, _E8M0, "b_scale", words * n * 4),
+                                at(bias, CBR_F32, "bias", n), at(d, s.d_type, "d", m * n), ws, nbytes, call.stream(stream)),
+           call.where)

@@ -11,7 +11,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libcbr.so")
 SOURCES = ["conv_fprop.hip", "conv_igemm.hip", "conv3x3_c64.hip", "conv_c3s2.hip", "bn_fwd.hip", "bn_bwd.hip",
            "conv_wgrad.hip", "cbr_api.cpp", "cbr_plan.cpp", "cbr_noalloc.hip", "block_norm_fwd.hip", "block_norm_bwd.hip",
-           "fp8_quant.hip", "fp8_gemm.hip", "block_api.cpp"]
+           "fp8_quant.hip", "fp8_gemm.hip", "block_api.cpp", "group_norm_fwd.hip", "group_norm_bwd.hip",
+           "group_norm_plan.cpp", "fp4_quant.hip", "fp4_gemm.hip", "more_api.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 # Packed fp32 instructions are disabled for device code (hipcc's host pass warns that

@@ -361,6 +361,121 @@ int cbr_gemm_fp8(const cbr_gemm_shape *shape, const void *a, const float *a_scal
                  void *workspace, size_t ws_bytes, void *stream);
 
 /*
+ * Group norm with an activation
+ * -----------------------------
+ * For maps that a convolution or a product left, where batches are too small for batch
+ * statistics: x [images][pixels][channels], dense (NHWC: pixels = H*W).  The channels are
+ * `groups` groups of channels / groups neighbouring ones; of each image's group
+ *   mean = mean of x, var = mean of (x - mean)^2 over pixels and channels (biased),
+ *   xhat = (x - mean) / sqrt(var + eps),  u = xhat * w_c + b_c,  y = act(u)
+ *   CBR_ACT_NONE: u;  CBR_ACT_RELU: max(u, 0), a NaN stays one;  CBR_ACT_SILU: u / (1 + e^-u).
+ * x, y, dx, dy have `type` (CBR_BF16, CBR_F16 or CBR_F32); w, b, their gradients and the
+ * statistics are float.  Everything is computed in fp32 and rounded once.
+ *
+ * Limits: channels a multiple of groups (CBR_E_SHAPE); channels / groups <= 8192, images and
+ * pixels < 2^31, at most 2^46 values, and not so many small groups or images that a launch
+ * would need 2^32 threads (CBR_E_UNSUPPORTED): 2^31 values are always fewer.
+ */
+enum cbr_act { CBR_ACT_NONE = 0, CBR_ACT_RELU = 1, CBR_ACT_SILU = 2 };
+
+typedef struct cbr_group_norm_shape {
+    int64_t images, pixels;
+    int32_t channels, groups;
+    int32_t type;                   /* enum cbr_dtype                                 */
+    int32_t act;                    /* enum cbr_act                                   */
+    float eps;
+} cbr_group_norm_shape;
+
+/* Workspace bytes of the forward (backward 0) or the backward (non-zero): 0 where the shape
+ * needs none, or is invalid.  Calls under way at the same time need one each. */
+size_t cbr_group_norm_workspace_bytes(const cbr_group_norm_shape *shape, int backward);
+
+/*
+ * Forward.  w, b [channels] may each be NULL (1, 0).  stats: float [images][groups][2], (mean,
+ * 1/sqrt(var + eps)), for the backward; NULL skips them (inference).  y may be x itself (in place);
+ * no other output may overlap an input.
+ */
+int cbr_group_norm_forward(const cbr_group_norm_shape *shape, const void *x, const float *w, const float *b,
+                           void *y, float *stats, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Backward.  dy: gradient to y; x, w, b and stats as the forward had and left them.  With
+ * g = dy * act'(u) (ReLU: 0 for u <= 0), over an image's pixels S1_c = sum g xhat, S0_c = sum g, and
+ * over a group of M = pixels * channels / groups values
+ *   dx = (w g - sum_c w S0 / M - xhat sum_c w S1 / M) / sqrt(var + eps),
+ *   dw = sum of S1 over the images,  db = sum of S0.
+ * dx, dw, db may each be NULL (not wanted), not all three.  dw needs no w, db no b.  The sums run in a fixed
+ * order: fp32 within an image's tile, fp64 beyond.  dx may be dy itself, or x (in place); no other
+ * output may overlap an input.
+ */
+int cbr_group_norm_backward(const cbr_group_norm_shape *shape, const void *dy, const void *x, const float *w,
+                            const float *b, const float *stats, void *dx, float *dw, float *db,
+                            void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * 4-bit floating point: operands with an exponent for each group of 32
+ * ---------------------------------------------------------------------
+ * src [rows][cols], dense, of CBR_BF16, CBR_F16 or CBR_F32; v is src, or its transpose
+ * where `transpose` is non-zero, with v_rows rows of v_cols values.  Each group of 32
+ * consecutive values of a row of v (fewer in a row's last one) has a scale, a power of two, and
+ * 4-bit values (sign, two bits of exponent, one of mantissa: 0, 1/2, 1, 3/2, 2, 3, 4, 6):
+ *   a = largest |v| of the group,  scale = 2^(floor(log2 a) - 2), at least 2^-127 (also a = 0),
+ *   q = v / scale, rounded to nearest, ties to even (0, 1, 2, 4), above 6 to 6.
+ * q [v_rows][ldq] bytes, two values a byte, the first in the lower four bits; ldq a
+ * multiple of 16, at least 16 * ceil(v_cols / 32): a group takes 16 bytes, zeros behind v_cols;
+ * bytes past the last group are left as they are.  scale: one byte a group, the exponent plus
+ * 127, [ceil(v_cols / 128)][v_rows][4]: the four groups of 128 values together; 127 (1) where
+ * there is no group.  A NaN or infinity makes its group's scale 255 (NaN) and its values 0: the
+ * group stands for NaN.  rows and cols positive, < 2^31, and
+ * ceil(rows / 64) * ceil(cols / 128) < 2^24 (CBR_E_UNSUPPORTED beyond that).  q and scale may
+ * not overlap src or each other.
+ */
+typedef struct cbr_fp4_shape {
+    int64_t rows, cols;             /* of src                                         */
+    int64_t ldq;                    /* bytes from a row of q to the next              */
+    int32_t type;                   /* of src: enum cbr_dtype                         */
+    int32_t transpose;
+} cbr_fp4_shape;
+
+int cbr_fp4_quantize(const cbr_fp4_shape *shape, const void *src, void *q, void *scale, void *stream);
+
+/* What q and scale stand for, in `type`: v [v_rows][v_cols], dense (of a transposed shape the transpose;
+ * it is not turned back).  Rounded to nearest where the type does not hold a value (CBR_F16).  v may not
+ * overlap q or scale. */
+int cbr_fp4_dequantize(const cbr_fp4_shape *shape, const void *q, const void *scale, void *v, void *stream);
+
+/*
+ * Matrix product of such operands:
+ *   d[i][j] = act( sum_t a_scale[i][t] * b_scale[j][t] * sum_{k in group t} a[i][k] * b[j][k]  + bias[j] )
+ * a [m][lda], b [n][ldb] bytes and scales [ceil(k / 128)][m or n][4] as cbr_fp4_quantize leaves them: the
+ * values behind k in the last group are part of the sum and have to be zeros (in one of the operands at
+ * least), what lies past the groups is not used.  lda, ldb multiples of 16, at least 16 * ceil(k / 32).
+ * d [m][n] dense, d_type CBR_BF16, CBR_F16 or CBR_F32; bias float [n] or NULL; act is max(v, 0) where relu
+ * is non-zero (a NaN stays one), else v.  All sums are fp32 (each matrix instruction of 128 values:
+ * within 2^-23 of the sum of magnitudes), and the result is rounded once.  A scaled sum that passes fp32's
+ * largest value within a group is an infinity, one below its smallest normal value may become 0.
+ * Forward, data and weight gradient of a 1x1 convolution as for cbr_gemm_fp8.
+ * m, n, k positive; m < 2^31, n, lda, ldb <= 2^22, k <= 2^23 and ceil(m / 64) * ceil(n / 64) <
+ * 2^24 - 1 (CBR_E_UNSUPPORTED beyond that).  d and the workspace may not overlap an operand or each other.
+ * The workspace (cbr_gemm_fp4_workspace_bytes, 0 where the shape needs none or is invalid) holds the parts
+ * of a long sum that several workgroups share; they are added in a fixed order.  Calls under way at the
+ * same time need one each.
+ */
+typedef struct cbr_gemm_fp4_shape {
+    int64_t m;
+    int64_t n, k;
+    int64_t lda, ldb;               /* bytes from a row to the next                   */
+    int32_t d_type;                 /* enum cbr_dtype                                 */
+    int32_t relu;
+} cbr_gemm_fp4_shape;
+
+size_t cbr_gemm_fp4_workspace_bytes(const cbr_gemm_fp4_shape *shape);
+
+int cbr_gemm_fp4(const cbr_gemm_fp4_shape *shape, const void *a, const void *a_scale, const void *b,
+                 const void *b_scale, const float *bias, void *d,
+                 void *workspace, size_t ws_bytes, void *stream);
+
+/*
  * Kernel plans (tuning interface).  Each convolution stage of a call runs one kernel and
  * tile shape, its "plan", chosen per shape like the per-shape engine choice of [CBR]
  * section 7 (empirical search, winner per shape) and [TL]'s autotuned tile

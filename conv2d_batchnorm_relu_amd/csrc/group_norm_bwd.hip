@@ -13,200 +13,325 @@ namespace {
 
 using namespace gnorm;
 
+// With d = x - mean: u = d a + b (SiLU: v = -log2(e) u, see scaled_sigmoid).
 template <int NV>
 struct Coef {
-    float mean[NV], inv[NV], w[8], b[8];
-    // of channel e: xhat, and g = dy act'(u)
-    __device__ __forceinline__ void grad(int e, float x, float dy, int act, float &xhat, float &g) const
+    float mean[NV], inv[NV], a[8], b[8];
+    // of channel e: d, and g = dy act'(u); SCALED: -ln 2 times that for SiLU, so that g times a is w g inv for all
+    template <bool SCALED>
+    __device__ __forceinline__ void grad(int e, float x, float dy, const Split<NV> &sp, int act, float &d, float &g) const
     {
-        const int s = NV == 1 ? 0 : e;
-        xhat = (x - mean[s]) * inv[s];
+        d = x - sp.pick(mean, e);
         if (act == CBR_ACT_NONE) {
             g = dy;
         } else {
-            const float u = fmaf(xhat, w[e], b[e]);
+            const float u = fmaf(d, a[e], b[e]);
             if (act == CBR_ACT_RELU) {
                 g = u > 0.f ? dy : u <= 0.f ? 0.f : u;   // a NaN stays one
             } else {
-                const float y = sigmoid(u);
-                g = dy * (y * fmaf(u, 1.f - y, 1.f));
+                const float s = scaled_sigmoid(u);   // -ln 2 sigmoid
+                // 1 + u (1 - sigmoid), with u = -ln 2 v
+                const float h = fmaf(u, -LN2 - s, 1.f);
+                g = dy * (SCALED ? s * h : (-LOG2E * s) * h);
             }
+        }
+    }
+    template <Tail TAIL>
+    __device__ __forceinline__ void load(const GroupNormArgs &p, const Place &at, const Thread &me, const Split<NV> &sp)
+    {
+        load_vec<8, TAIL>(p.w ? p.w + at.c0 : nullptr, 1.f, me.vec, p.g.V, at.w, a);
+        load_vec<8, TAIL>(p.b ? p.b + at.c0 : nullptr, 0.f, me.vec, p.g.V, at.w, b);
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+            const f32x2 st = me.image < p.images ? *(const f32x2 *)(p.stats_in + (me.image * p.G + at.chunk * p.g.ng + sp.gi[e]) * 2) : f32x2{0.f, 0.f};
+            mean[e] = st[0];
+            inv[e] = st[1];
+        }
+        const float c = p.act == CBR_ACT_SILU ? -LOG2E : 1.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            a[e] *= sp.pick(inv, e) * c;
+            b[e] *= c;
         }
     }
 };
 
-// TILES: leaves the tile's S1 and S0 of each channel; else also dx.
-template <typename T, Tail TAIL, int NV, int K, bool TILES>
-__global__ __launch_bounds__(1024) void gn_bwd_kernel(GroupNormArgs p)
+// A pixel added to a thread's sums of g d and g for each channel.
+template <typename T, int NV>
+__device__ __forceinline__ void add_pixel(const Coef<NV> &cf, const Raw8<T> &rx, const Raw8<T> &rd, const Split<NV> &sp, int act, float (&s1)[8], float (&s0)[8])
 {
-    extern __shared__ __attribute__((aligned(16))) float lds[];
-    const Place<false> at(p, gridDim.x);
-    const Geo &g = p.g;
-    const int t = threadIdx.x, vec = t % g.V, q = t / g.V, prow = q % g.P, sub = q / g.P;
-    const int64_t image = at.image + sub, first = (int64_t)at.tile * g.P * g.k;
-    const int64_t rows = min((int64_t)g.P * g.k, p.pixels - first);
-    const bool on = image < p.images;
-    const int left = (int)(rows - prow);
-    const int64_t start = ((image * p.pixels + first + prow) * p.C + at.c0) * T::SIZE, step = (int64_t)g.P * p.C * T::SIZE;
-    Row<T, 8, TAIL> rx[K], rd[K];
+    float x[8], dy[8];
+    unpack8<T>(rx, x);
+    unpack8<T>(rd, dy);
 #pragma unroll
-    for (int i = 0; i < K; ++i)
-        if (i < g.k) {
-            rx[i].load((const char *)p.x + start + i * step, vec, g.V, at.w, on && i * g.P < left);
-            rd[i].load((const char *)p.dy + start + i * step, vec, g.V, at.w, on && i * g.P < left);
-        }
-    Coef<NV> cf;
-    load_vec<8, TAIL>(p.w ? p.w + at.c0 : nullptr, 1.f, vec, g.V, at.w, cf.w);
-    load_vec<8, TAIL>(p.b ? p.b + at.c0 : nullptr, 0.f, vec, g.V, at.w, cf.b);
-    int gi[NV];
-    groups_of<NV>(vec, p.cpg, at.ngl, gi);
-#pragma unroll
-    for (int e = 0; e < NV; ++e) {
-        const f32x2 st = on ? *(const f32x2 *)(p.stats_in + (image * p.G + at.chunk * g.ng + gi[e]) * 2) : f32x2{0.f, 0.f};
-        cf.mean[e] = st[0];
-        cf.inv[e] = st[1];
-    }
-    float s1[8] = {}, s0[8] = {};
-#pragma unroll
-    for (int i = 0; i < K; ++i)
-        if (i < g.k && i * g.P < left) {
-            float x[8], d[8];
-            rx[i].get(x, vec, g.V, at.w);
-            rd[i].get(d, vec, g.V, at.w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float xhat, gr;
-                cf.grad(e, x[e], d[e], p.act, xhat, gr);
-                s0[e] += gr;
-                s1[e] = fmaf(gr, xhat, s1[e]);
-            }
-        }
-    // Over the pixels: within the waves, then through LDS in a fixed order
-    const int wd = 8 * g.V * g.ipw, nrows = g.pre ? g.P * g.V / 64 : g.P;
-    float *const red = lds, *const col = red + 2 * nrows * wd, *const tot = col + 2 * wd;   // [2] of each
-    {
-        if (g.pre) add_same<8>(s1, s0, g.V);
-        const int row = g.pre ? prow * g.V / 64 : prow, c = (sub * g.V + vec) * 8;
-        if (!g.pre || (t & 63) < g.V)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                red[2 * row * wd + c + e] = s1[e];
-                red[(2 * row + 1) * wd + c + e] = s0[e];
-            }
-    }
-    __syncthreads();
-    for (int c = t; c < 2 * wd; c += blockDim.x) {
-        float v = 0.f;
-        for (int r = 0; r < nrows; ++r) v += red[2 * r * wd + c];
-        // column c of a sum: image c / (8 V), channel c % (8 V) of the chunk
-        const int s = c >= wd, cc = c - s * wd, im = cc / (8 * g.V), ch = cc % (8 * g.V);
-        if (ch < at.w && at.image + im < p.images) {
-            // one image and one tile: these are the gradients; else parts of them
-            if (p.part) p.part[(((at.image + im) * g.tiles + at.tile) * 2 + s) * p.C + at.c0 + ch] = v;
-            else if (float *o = s ? p.db : p.dw) o[at.c0 + ch] = v;
-            if constexpr (!TILES) col[c] = v * (p.w ? p.w[at.c0 + ch] : 1.f);
-        }
-    }
-    if constexpr (!TILES) {
-        if (!p.out) return;
-        __syncthreads();
-        columns_to_groups(col, tot, p.cpg, 8 * g.V, g.ng, g.ipw);
-        columns_to_groups(col + wd, tot + g.ng * g.ipw, p.cpg, 8 * g.V, g.ng, g.ipw);
-        __syncthreads();
-        const float m = 1.f / ((float)p.pixels * (float)p.cpg);
-        float m1[NV], m0[NV];
-#pragma unroll
-        for (int e = 0; e < NV; ++e) {
-            m1[e] = tot[sub * g.ng + gi[e]] * m;
-            m0[e] = tot[g.ng * g.ipw + sub * g.ng + gi[e]] * m;
-        }
-#pragma unroll
-        for (int i = 0; i < K; ++i)
-            if (i < g.k && on && i * g.P < left) {
-                float x[8], d[8];
-                rx[i].get(x, vec, g.V, at.w);
-                rd[i].get(d, vec, g.V, at.w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float xhat, gr;
-                    const int z = NV == 1 ? 0 : e;
-                    cf.grad(e, x[e], d[e], p.act, xhat, gr);
-                    x[e] = (fmaf(gr, cf.w[e], -m0[z]) - xhat * m1[z]) * cf.inv[z];
-                }
-                Row<T, 8, TAIL>::store((char *)p.out + start + i * step, vec, g.V, at.w, x);
-            }
+    for (int e = 0; e < 8; ++e) {
+        float d, g;
+        cf.template grad<false>(e, x[e], dy[e], sp, act, d, g);
+        s0[e] += g;
+        s1[e] = fmaf(g, d, s1[e]);
     }
 }
 
-// dw, db of 64 channels from c0 on: the images' and tiles' parts added in fp64, in a fixed order.
-__device__ __forceinline__ void finish(const GroupNormArgs &p, int c0, double *lds)
+// dx of a pixel's eight channels: w g inv - c0 - d c1.
+template <typename T, int NV>
+__device__ __forceinline__ void dx_of(const Coef<NV> &cf, const Raw8<T> &rx, const Raw8<T> &rd, const Split<NV> &sp, int act, const float (&c1)[NV],
+                                      const float (&c0)[NV], float (&x)[8])
 {
-    const int c = c0 + (threadIdx.x & 63), wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int64_t rows = p.images * p.g.tiles;
-    double s1 = 0., s0 = 0.;
-    if (c < p.C && wave < waves)
-        for (int64_t r = wave; r < rows; r += waves) {
-            s1 += p.part[2 * r * p.C + c];
-            s0 += p.part[(2 * r + 1) * p.C + c];
+    float dy[8];
+    unpack8<T>(rx, x);
+    unpack8<T>(rd, dy);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float d, g;
+        cf.template grad<true>(e, x[e], dy[e], sp, act, d, g);
+        x[e] = fmaf(g, cf.a[e], fmaf(-sp.pick(c1, e), d, -sp.pick(c0, e)));
+    }
+}
+
+// A thread's S1 and S0 added within its wave and left in LDS: rows [2][8 V ipw].
+__device__ __forceinline__ void leave_channels(const Geo &g, const Thread &me, float (&s1)[8], float (&s0)[8], float *red)
+{
+    const int wd = 8 * g.V * g.ipw;
+    if (g.pre) add_same<8>(s1, s0, g.V);
+    const int row = g.pre ? me.prow * g.V / 64 : me.prow, c = (me.sub * g.V + me.vec) * 8;
+    if (!g.pre || (threadIdx.x & 63) < (unsigned)g.V)
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+            *(f32x4 *)(red + 2 * row * wd + c + e) = f32x4{s1[e], s1[e + 1], s1[e + 2], s1[e + 3]};
+            *(f32x4 *)(red + (2 * row + 1) * wd + c + e) = f32x4{s0[e], s0[e + 1], s0[e + 2], s0[e + 3]};
         }
-    lds[2 * threadIdx.x] = s1;
-    lds[2 * threadIdx.x + 1] = s0;
+}
+
+// Behind a barrier: the columns' sums in a fixed order; `use` is called with the sum, which of the two it is, the image
+// and the channel of the chunk.
+template <typename F>
+__device__ __forceinline__ void take_channels(const Geo &g, const float *red, F &&use)
+{
+    const int wd = 8 * g.V * g.ipw, rows = sum_rows(g);
+    for (int i = threadIdx.x; i < 2 * wd; i += blockDim.x) {
+        float v = 0.f;
+        for (int r = 0; r < rows; ++r) v += red[2 * r * wd + i];
+        const int s = i >= wd, j = i - s * wd;
+        use(v, s, j / (8 * g.V), j % (8 * g.V));
+    }
+}
+
+// Images held whole.
+template <typename T, Tail TAIL, int NV, int K>
+__global__ __launch_bounds__(1024) void gn_bwd_kernel(GroupNormArgs p)
+{
+    extern __shared__ __attribute__((aligned(16))) float lds[];
+    const Place at(p);
+    const Geo &g = p.g;
+    const Thread me(p, at);
+    const int row = me.sub * (int)p.pixels + me.prow;
+    const Part<T, TAIL> ix(p.x, me.first, row, p.C, g.P, me.vec, at.w), id(p.dy, me.first, row, p.C, g.P, me.vec, at.w);
+    Raw8<T> rx[K], rd[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+        if (i < g.k) {
+            ix.load(rx[i], i, i * g.P < me.left);
+            id.load(rd[i], i, i * g.P < me.left);
+        }
+    const Split<NV> sp(me.vec, p.cpg, at.ngl);
+    Coef<NV> cf;
+    cf.template load<TAIL>(p, at, me, sp);
+    float *const channels = lds + 2 * 2 * sum_rows(g) * NV * g.V * g.ipw + 2 * (NV * g.V * g.ipw + g.ng * g.ipw);   // behind the groups' sums
+    float s[2][NV];
+    {
+        float s1[8] = {}, s0[8] = {};
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (i < g.k && i * g.P < me.left) {
+                ix.settle(rx[i]);
+                id.settle(rd[i]);
+                add_pixel<T, NV>(cf, rx[i], rd[i], sp, p.act, s1, s0);
+            }
+        // The groups' sums of w g xhat and w g (a is w inv, times SiLU's constant: see below), beside the channels'
+        float t1[8], t0[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const bool real = TAIL == WHOLE || 8 * me.vec + e < at.w;
+            t1[e] = real ? cf.a[e] * s1[e] : 0.f;
+            t0[e] = real ? cf.a[e] * s0[e] : 0.f;
+            s1[e] *= sp.pick(cf.inv, e);
+        }
+        sp.collapse(t1, s[0]);
+        sp.collapse(t0, s[1]);
+        leave_channels(g, me, s1, s0, channels);
+    }
+    GroupSum<NV, 2> sum(p, lds, me);
+    sum(s, sp);
+    if (p.out) {
+        const float m = (p.act == CBR_ACT_SILU ? -LN2 : 1.f) / ((float)p.pixels * (float)p.cpg);
+        float c1[NV], c0[NV];   // inv^2 mean(w g xhat), inv mean(w g)
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+            c1[e] = s[0][e] * m * cf.inv[e] * cf.inv[e];
+            c0[e] = s[1][e] * m;
+        }
+        const Part<T, TAIL> out(p.out, me.first, row, p.C, g.P, me.vec, at.w);
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (i < g.k) {
+                float x[8];
+                dx_of<T, NV>(cf, rx[i], rd[i], sp, p.act, c1, c0, x);
+                out.store(x, i, i * g.P < me.left, p.nt);
+            }
+    }
+    // Beside the stores: a single image's sums are the gradients, others parts of them
+    take_channels(g, channels, [&](float v, int i, int im, int ch) __attribute__((always_inline)) {
+        if (ch >= at.w || at.image + im >= p.images) return;
+        if (p.part) p.part[((at.image + im) * 2 + i) * p.C + at.c0 + ch] = v;
+        else if (float *o = i ? p.db : p.dw) o[at.c0 + ch] = v;
+    });
+}
+
+// K of a thread's pixels of x and dy.
+template <typename T, Tail TAIL, int K>
+struct Pair {
+    Raw8<T> x[K], d[K];
+    __device__ __forceinline__ void fetch(const Part<T, TAIL> &ix, const Part<T, TAIL> &id, const Geo &g, const Thread &me, int i0)
+    {
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const bool on = (i0 + i) * g.P < me.left && i0 + i < g.k;
+            ix.load(x[i], i0 + i, on);
+            id.load(d[i], i0 + i, on);
+        }
+    }
+    __device__ __forceinline__ void settle(const Part<T, TAIL> &ix)
+    {
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            ix.settle(x[i]);
+            ix.settle(d[i]);
+        }
+    }
+};
+
+// First kernel of large images: a tile's S1 and S0 of each channel.
+template <typename T, Tail TAIL, int NV, int K>
+__global__ __launch_bounds__(1024) void gn_bwd_tiles_kernel(GroupNormArgs p)
+{
+    extern __shared__ __attribute__((aligned(16))) float lds[];
+    const Place at(p);
+    const Geo &g = p.g;
+    const Thread me(p, at);
+    const Part<T, TAIL> ix(p.x, me.first, me.prow, p.C, g.P, me.vec, at.w), id(p.dy, me.first, me.prow, p.C, g.P, me.vec, at.w);
+    const Split<NV> sp(me.vec, p.cpg, at.ngl);
+    Pair<T, TAIL, K> one, two;
+    one.fetch(ix, id, g, me, 0);   // one turn is on its way while the other is added
+    Coef<NV> cf;
+    cf.template load<TAIL>(p, at, me, sp);
+    float s1[8] = {}, s0[8] = {};
+    auto add = [&](Pair<T, TAIL, K> &r, int i0) __attribute__((always_inline)) {
+        r.settle(ix);
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if ((i0 + i) * g.P < me.left && i0 + i < g.k) add_pixel<T, NV>(cf, r.x[i], r.d[i], sp, p.act, s1, s0);
+    };
+    for (int i0 = 0; i0 < g.k; i0 += 2 * K) {
+        two.fetch(ix, id, g, me, i0 + K);
+        add(one, i0);
+        one.fetch(ix, id, g, me, i0 + 2 * K);
+        add(two, i0 + K);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s1[e] *= sp.pick(cf.inv, e);
+    leave_channels(g, me, s1, s0, lds);
     __syncthreads();
-    if (threadIdx.x < 64 && c < p.C) {
-        for (int i = 1; i < waves; ++i) {
-            s1 += lds[2 * (threadIdx.x + 64 * i)];
-            s0 += lds[2 * (threadIdx.x + 64 * i) + 1];
+    take_channels(g, lds, [&](float v, int i, int, int ch) __attribute__((always_inline)) {
+        if (ch < at.w) p.part[((me.image * g.tiles + at.tile) * 2 + i) * p.C + at.c0 + ch] = v;
+    });
+}
+
+// dw, db of FC channels a workgroup: the images' and tiles' parts added in fp64, in a fixed order, by rows of FC
+// threads (64 channels a workgroup left one to read 2 MB: 12.9 us of 8 x 50176 x 64; 16: 5).
+constexpr int FC = 16;
+
+__global__ __launch_bounds__(1024) void gn_bwd_finish_kernel(GroupNormArgs p)
+{
+    extern __shared__ __attribute__((aligned(16))) double sums[];   // [rows of threads][FC][2]
+    const int c = blockIdx.x * FC + (threadIdx.x % FC), lane = threadIdx.x / FC, lanes = blockDim.x / FC;
+    const int64_t rows = p.images * p.g.tiles, ld = 2 * (int64_t)p.C;
+    double s1 = 0., s0 = 0.;
+    if (c < p.C) {
+        const float *q = p.part + c;
+        int64_t r = lane;
+        for (; r + 7 * lanes < rows; r += 8 * lanes) {   // sixteen loads under way
+            float v[8], w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = q[(r + i * lanes) * ld];
+                w[i] = q[(r + i * lanes) * ld + p.C];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s1 += v[i];
+                s0 += w[i];
+            }
         }
+        for (; r < rows; r += lanes) {
+            s1 += q[r * ld];
+            s0 += q[r * ld + p.C];
+        }
+    }
+    sums[2 * threadIdx.x] = s1;
+    sums[2 * threadIdx.x + 1] = s0;
+    for (int n = lanes / 2; n > 0; n /= 2) {   // (lanes: a power of two)
+        __syncthreads();
+        if (lane < n) {
+            s1 += sums[2 * (threadIdx.x + n * FC)];
+            s0 += sums[2 * (threadIdx.x + n * FC) + 1];
+            sums[2 * threadIdx.x] = s1;
+            sums[2 * threadIdx.x + 1] = s0;
+        }
+    }
+    if (lane == 0 && c < p.C) {
         if (p.dw) p.dw[c] = (float)s1;
         if (p.db) p.db[c] = (float)s0;
     }
 }
 
-__global__ __launch_bounds__(1024) void gn_bwd_finish_kernel(GroupNormArgs p)
-{
-    extern __shared__ __attribute__((aligned(16))) float lds[];
-    finish(p, blockIdx.x * 64, (double *)lds);
-}
+// Second kernel of large images: the tiles' sums joined, then the tile's dx.  LDS (floats): [parts][2][8 V] sums of some
+// tiles, [2][8 V] columns, [2][ng] groups.
+inline __host__ __device__ int apply_parts(const Geo &g) { return max(1, min(g.V * g.P / (16 * g.V), 8)); }
+inline int apply_floats(const Geo &g) { return 16 * g.V * (apply_parts(g) + 1) + 2 * g.ng; }
 
-// Second kernel of large images: the tiles' sums joined, then the tile's dx.
 template <typename T, Tail TAIL, int NV, int K>
 __global__ __launch_bounds__(1024) void gn_bwd_apply_kernel(GroupNormArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) float lds[];
+    const Place at(p);
     const Geo &g = p.g;
-    const Place<true> at(p, gridDim.x);
-    const int t = threadIdx.x, vec = t % g.V, prow = t / g.V;
-    const int64_t image = at.image, per_tile = (int64_t)g.P * g.k, first = at.tile * per_tile;
-    const int64_t rows = min(per_tile, p.pixels - first);
-    const int left = (int)(rows - prow);
-    const int64_t start = ((image * p.pixels + first + prow) * p.C + at.c0) * T::SIZE, step = (int64_t)g.P * p.C * T::SIZE;
-    Row<T, 8, TAIL> rx[K], rd[K];
-#pragma unroll
-    for (int i = 0; i < K; ++i)
-        if (i < g.k) {
-            rx[i].load((const char *)p.x + start + i * step, vec, g.V, at.w, i * g.P < left);
-            rd[i].load((const char *)p.dy + start + i * step, vec, g.V, at.w, i * g.P < left);
-        }
+    const Thread me(p, at);
+    const Part<T, TAIL> ix(p.x, me.first, me.prow, p.C, g.P, me.vec, at.w), id(p.dy, me.first, me.prow, p.C, g.P, me.vec, at.w),
+        out(p.out, me.first, me.prow, p.C, g.P, me.vec, at.w);
+    Pair<T, TAIL, K> one, two;
+    one.fetch(ix, id, g, me, 0);
+    const Split<NV> sp(me.vec, p.cpg, at.ngl);
     Coef<NV> cf;
-    load_vec<8, TAIL>(p.w ? p.w + at.c0 : nullptr, 1.f, vec, g.V, at.w, cf.w);
-    load_vec<8, TAIL>(p.b ? p.b + at.c0 : nullptr, 0.f, vec, g.V, at.w, cf.b);
-    int gi[NV];
-    groups_of<NV>(vec, p.cpg, at.ngl, gi);
-#pragma unroll
-    for (int e = 0; e < NV; ++e) {
-        const f32x2 st = *(const f32x2 *)(p.stats_in + (image * p.G + at.chunk * g.ng + gi[e]) * 2);
-        cf.mean[e] = st[0];
-        cf.inv[e] = st[1];
-    }
+    cf.template load<TAIL>(p, at, me, sp);
     // The tiles' sums of the chunk's channels, added in a fixed order by some threads a channel
-    const int wd = 8 * g.V, parts = max(1, min((int)blockDim.x / (2 * wd), 8));
+    const int t = threadIdx.x, wd = 8 * g.V, parts = apply_parts(g);
     float *const red = lds, *const col = red + 2 * wd * parts, *const tot = col + 2 * wd;
     for (int i = t; i < 2 * wd * parts; i += blockDim.x) {
         const int c = i % (2 * wd), s = c >= wd, ch = c - s * wd;
         float v = 0.f;
-        if (ch < at.w)
-            for (int r = i / (2 * wd); r < g.tiles; r += parts)
-                v += p.part[((image * g.tiles + r) * 2 + s) * p.C + at.c0 + ch];
+        if (ch < at.w) {
+            const float *q = p.part + (me.image * g.tiles * 2 + s) * p.C + at.c0 + ch;
+            const int64_t ld = 2 * (int64_t)p.C;
+            int r = i / (2 * wd);
+            for (; r + 7 * parts < g.tiles; r += 8 * parts) {   // eight loads under way
+                float w[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) w[u] = q[(r + u * parts) * ld];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v += w[u];
+            }
+            for (; r < g.tiles; r += parts) v += q[r * ld];
+        }
         red[i] = v;
     }
     __syncthreads();
@@ -217,74 +342,74 @@ __global__ __launch_bounds__(1024) void gn_bwd_apply_kernel(GroupNormArgs p)
         if (ch < at.w) col[c] = v * (p.w ? p.w[at.c0 + ch] : 1.f);
     }
     __syncthreads();
-    columns_to_groups(col, tot, p.cpg, wd, g.ng, 1);
-    columns_to_groups(col + wd, tot + g.ng, p.cpg, wd, g.ng, 1);
+    columns_to_groups<8>(col, tot, p.cpg, wd, at.ngl, 1);
+    columns_to_groups<8>(col + wd, tot + g.ng, p.cpg, wd, at.ngl, 1);
     __syncthreads();
     const float m = 1.f / ((float)p.pixels * (float)p.cpg);
-    float m1[NV], m0[NV];
+    float c1[NV], c0[NV];
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
-        m1[e] = tot[gi[e]] * m;
-        m0[e] = tot[g.ng + gi[e]] * m;
+        c1[e] = tot[sp.gi[e]] * m * cf.inv[e] * cf.inv[e];
+        c0[e] = tot[g.ng + sp.gi[e]] * m * cf.inv[e];
     }
+    auto finish = [&](Pair<T, TAIL, K> &r, int i0) __attribute__((always_inline)) {
+        r.settle(ix);
 #pragma unroll
-    for (int i = 0; i < K; ++i)
-        if (i < g.k && i * g.P < left) {
-            float x[8], d[8];
-            rx[i].get(x, vec, g.V, at.w);
-            rd[i].get(d, vec, g.V, at.w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float xhat, gr;
-                const int z = NV == 1 ? 0 : e;
-                cf.grad(e, x[e], d[e], p.act, xhat, gr);
-                x[e] = (fmaf(gr, cf.w[e], -m0[z]) - xhat * m1[z]) * cf.inv[z];
-            }
-            Row<T, 8, TAIL>::store((char *)p.out + start + i * step, vec, g.V, at.w, x);
+        for (int i = 0; i < K; ++i) {
+            float x[8];
+            dx_of<T, NV>(cf, r.x[i], r.d[i], sp, p.act, c1, c0, x);
+            out.store(x, i0 + i, (i0 + i) * g.P < me.left && i0 + i < g.k, p.nt);
         }
+    };
+    for (int i0 = 0; i0 < g.k; i0 += 2 * K) {
+        two.fetch(ix, id, g, me, i0 + K);
+        finish(one, i0);
+        one.fetch(ix, id, g, me, i0 + 2 * K);
+        finish(two, i0 + K);
+    }
 }
 
-template <typename T, Tail TAIL, int NV, int K>
-hipError_t launch_k(const GroupNormArgs &a, hipStream_t st)
+template <typename Kern>
+hipError_t launch_with(Kern k, const GroupNormArgs &a, int lds, hipStream_t st)
 {
     const Geo &g = a.g;
     const uint32_t grid = (uint32_t)((a.images + g.ipw - 1) / g.ipw * g.tiles * g.chunks);
-    const int lds = lds_floats(g, 8, 2) * (int)sizeof(float), threads = g.V * g.P * g.ipw;
-    auto k = g.tiles == 1 ? gn_bwd_kernel<T, TAIL, NV, K, false> : gn_bwd_kernel<T, TAIL, NV, K, true>;
-    hipError_t e = raise_lds_limit((const void *)k, lds);
-    if (e == hipSuccess) e = launch(k, dim3(grid), dim3(threads), lds, st, nullptr, nullptr, a);
+    const hipError_t e = raise_lds_limit((const void *)k, lds);
     if (e != hipSuccess) return e;
-    if (g.tiles > 1 && a.out) {
-        auto k2 = gn_bwd_apply_kernel<T, TAIL, NV, K>;
-        const int wd = 8 * g.V, parts = std::max(1, std::min(threads / (2 * wd), 8));
-        const int lds2 = (2 * wd * (parts + 1) + 2 * g.ng) * (int)sizeof(float);
-        e = raise_lds_limit((const void *)k2, lds2);
-        if (e == hipSuccess) e = launch(k2, dim3(grid), dim3(threads), lds2, st, nullptr, nullptr, a);
-        if (e != hipSuccess) return e;
-    }
-    if (a.part && (a.dw || a.db)) {
-        const int n = a.images * g.tiles >= 64 ? 1024 : 256;
-        return launch(gn_bwd_finish_kernel, dim3((a.C + 63) / 64), dim3(n), n * 16, st, nullptr, nullptr, a);
-    }
-    return hipSuccess;
+    return launch(k, dim3(grid), dim3(threads_of(g)), lds, st, nullptr, nullptr, a);
 }
 
 template <typename T, Tail TAIL, int NV>
 hipError_t launch_tail(const GroupNormArgs &a, hipStream_t st)
 {
-    constexpr int B = 4 / T::SIZE;
-    if (a.g.k <= B) return launch_k<T, TAIL, NV, B>(a, st);
-    if (a.g.k <= 3 * B) return launch_k<T, TAIL, NV, 3 * B>(a, st);
-    return launch_k<T, TAIL, NV, 6 * B>(a, st);
+    constexpr int B = 4 / T::SIZE, TURN = bwd_turn(NV) * B;
+    const Geo &g = a.g;
+    const int lds = bwd_floats(g, a.cpg) * (int)sizeof(float);
+    hipError_t e;
+    if (g.tiles > 1) {
+        e = launch_with(gn_bwd_tiles_kernel<T, TAIL, NV, TURN>, a, lds, st);
+        if (e == hipSuccess && a.out)
+            e = launch_with(gn_bwd_apply_kernel<T, TAIL, NV, TURN>, a, apply_floats(g) * (int)sizeof(float), st);
+    } else if (g.k <= B) {
+        e = launch_with(gn_bwd_kernel<T, TAIL, NV, B>, a, lds, st);
+    } else if (g.k <= 2 * B) {
+        e = launch_with(gn_bwd_kernel<T, TAIL, NV, 2 * B>, a, lds, st);
+    } else {
+        e = launch_with(gn_bwd_kernel<T, TAIL, NV, bwd_most(NV) * B>, a, lds, st);
+    }
+    if (e != hipSuccess || !a.part || !(a.dw || a.db)) return e;
+    const int n = a.images * g.tiles >= 64 ? 1024 : 256;
+    return launch(gn_bwd_finish_kernel, dim3((a.C + FC - 1) / FC), dim3(n), n * 16, st, nullptr, nullptr, a);
 }
 
 template <typename T>
 hipError_t launch_type(const GroupNormArgs &a, hipStream_t st)
 {
     if (a.cpg % 8 == 0) return launch_tail<T, WHOLE, 1>(a, st);
-    if (a.C % 8 == 0 && a.g.ng * a.cpg % 8 == 0) return launch_tail<T, WHOLE, 8>(a, st);
-    if (a.C >= 8) return launch_tail<T, PART, 8>(a, st);
-    return launch_tail<T, SHORT, 8>(a, st);   // (one chunk)
+    const bool whole = a.C % 8 == 0 && (a.g.chunks == 1 || a.g.ng * a.cpg % 8 == 0);
+    if (a.cpg > 8) return whole ? launch_tail<T, WHOLE, 2>(a, st) : launch_tail<T, PART, 2>(a, st);
+    if (whole) return launch_tail<T, WHOLE, 8>(a, st);
+    return a.C >= 8 ? launch_tail<T, PART, 8>(a, st) : launch_tail<T, SHORT, 8>(a, st);   // (shorter: one chunk)
 }
 
 }  // namespace

@@ -3,7 +3,7 @@
 // A workgroup holds whole groups of an image in registers from the load to the store, so x is read
 // once, and the squared deviations are summed after the mean (no difference of large sums).  Where an
 // image is too large for that, one kernel leaves every tile's (mean, M2), joined exactly by the
-// formula of Chan, Golub and LeVeque, and a second one reads x again, last tile first.
+// formula of Chan, Golub and LeVeque, and a second one reads x again.
 #include "block_launch.h"
 #include "group_norm.h"
 
@@ -12,102 +12,191 @@ namespace {
 
 using namespace gnorm;
 
-template <Tail TAIL, int NV>
+template <int NV>
 struct Coef {
-    float mean[NV], a[8], b[8];   // y = act((x - mean) a + b)
-    __device__ __forceinline__ void apply(float (&v)[8], int act) const
+    float mean[NV], a[8], b[8];   // u = (x - mean) a + b; SiLU: -log2(e) times that
+    // a, b: w and b as they were given
+    __device__ __forceinline__ void set(const float (&inv)[NV], const Split<NV> &sp, int act)
+    {
+        const float c = act == CBR_ACT_SILU ? -LOG2E : 1.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            a[e] *= sp.pick(inv, e) * c;
+            b[e] *= c;
+        }
+    }
+    __device__ __forceinline__ void apply(float (&v)[8], const Split<NV> &sp, int act) const
     {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e] - mean[NV == 1 ? 0 : e], a[e], b[e]);
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e] - sp.pick(mean, e), a[e], b[e]);
         if (act == CBR_ACT_RELU) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = v[e] < 0.f ? 0.f : v[e];   // a NaN stays one
         } else if (act == CBR_ACT_SILU) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= sigmoid(v[e]);
+            for (int e = 0; e < 8; ++e) v[e] *= scaled_sigmoid(v[e]);
         }
     }
 };
 
-// TILES: leaves each group's (mean, M2) of this tile instead of y.
-template <typename T, Tail TAIL, int NV, int K, bool TILES>
+// The thread of a group's first channel and pixel leaves its two values at out[group * stride].
+template <int NV>
+__device__ __forceinline__ void leave_groups(const GroupNormArgs &p, const Place &at, const Thread &me, const Split<NV> &sp, float *out,
+                                             int64_t stride, const float (&u)[NV], const float (&v)[NV])
+{
+    if (me.prow == 0 && me.on)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = 8 * me.vec + e;
+            if (c < at.w && c % p.cpg == 0) *(f32x2 *)(out + c / p.cpg * stride) = f32x2{sp.pick(u, e), sp.pick(v, e)};
+        }
+}
+
+// Images held whole.
+template <typename T, Tail TAIL, int NV, int K>
 __global__ __launch_bounds__(1024) void gn_fwd_kernel(GroupNormArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) float lds[];
-    const Place<false> at(p, gridDim.x);
+    const Place at(p);
     const Geo &g = p.g;
-    const int t = threadIdx.x, vec = t % g.V, q = t / g.V, prow = q % g.P, sub = q / g.P;
-    const int64_t image = at.image + sub, first = (int64_t)at.tile * g.P * g.k;
-    const int64_t rows = min((int64_t)g.P * g.k, p.pixels - first);   // of this tile
-    const bool on = image < p.images;
-    const int left = (int)(rows - prow);                               // pixels prow, prow + P, ... below it
-    const int64_t start = ((image * p.pixels + first + prow) * p.C + at.c0) * T::SIZE, step = (int64_t)g.P * p.C * T::SIZE;
-    Row<T, 8, TAIL> raw[K];
+    const Thread me(p, at);
+    const int row = me.sub * (int)p.pixels + me.prow;
+    const Part<T, TAIL> in(p.x, me.first, row, p.C, g.P, me.vec, at.w);
+    Raw8<T> raw[K];
 #pragma unroll
     for (int i = 0; i < K; ++i)
-        if (i < g.k) raw[i].load((const char *)p.x + start + i * step, vec, g.V, at.w, on && i * g.P < left);
-    Coef<TAIL, NV> cf;
-    if constexpr (!TILES) {
-        load_vec<8, TAIL>(p.w ? p.w + at.c0 : nullptr, 1.f, vec, g.V, at.w, cf.a);
-        load_vec<8, TAIL>(p.b ? p.b + at.c0 : nullptr, 0.f, vec, g.V, at.w, cf.b);
-    }
-    GroupSum<NV> sum(p, lds, vec, prow, sub);
-    int gi[NV];
-    groups_of<NV>(vec, p.cpg, at.ngl, gi);
-    const float count = (float)rows * (float)p.cpg;
-
-    float s[NV] = {};
+        if (i < g.k) in.load(raw[i], i, i * g.P < me.left);
+    GroupSum<NV, 1> sum(p, lds, me);
+    const Split<NV> sp(me.vec, p.cpg, at.ngl);
+    const float count = (float)p.pixels * (float)p.cpg;
+    Coef<NV> cf;
+    float c[8] = {}, s[1][NV];
 #pragma unroll
     for (int i = 0; i < K; ++i)
         if (i < g.k) {   // (what is not there was loaded as zeros)
             float v[8];
-            raw[i].get(v, vec, g.V, at.w);
+            in.settle(raw[i]);
+            unpack8<T>(raw[i], v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[NV == 1 ? 0 : e] += v[e];
+            for (int e = 0; e < 8; ++e) c[e] += v[e];
         }
-    sum(s, gi);
+    sp.collapse(c, s[0]);
+    sum(s, sp);
 #pragma unroll
-    for (int e = 0; e < NV; ++e) {
-        cf.mean[e] = s[e] / count;
-        s[e] = 0.f;
-    }
+    for (int e = 0; e < NV; ++e) cf.mean[e] = s[0][e] / count;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+        if (i < g.k && i * g.P < me.left) {
+            float v[8];
+            unpack8<T>(raw[i], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = v[e] - sp.pick(cf.mean, e);
+                c[e] = fmaf(d, d, c[e]);
+            }
+        }
+    if (TAIL != WHOLE)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = 8 * me.vec + e < at.w ? c[e] : 0.f;
+    // (asked for beside the second sum)
+    load_vec<8, TAIL>(p.w ? p.w + at.c0 : nullptr, 1.f, me.vec, g.V, at.w, cf.a);
+    load_vec<8, TAIL>(p.b ? p.b + at.c0 : nullptr, 0.f, me.vec, g.V, at.w, cf.b);
+    sp.collapse(c, s[0]);
+    sum(s, sp);
+#pragma unroll
+    for (int e = 0; e < NV; ++e) s[0][e] = 1.f / sqrtf(s[0][e] / count + p.eps);
+    if (p.stats) leave_groups<NV>(p, at, me, sp, p.stats + (me.image * p.G + at.chunk * g.ng) * 2, 2, cf.mean, s[0]);
+    cf.set(s[0], sp, p.act);
+    const Part<T, TAIL> out(p.out, me.first, row, p.C, g.P, me.vec, at.w);
 #pragma unroll
     for (int i = 0; i < K; ++i)
         if (i < g.k) {
-            float v[8], u[NV] = {};
-            raw[i].get(v, vec, g.V, at.w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float d = v[e] - cf.mean[NV == 1 ? 0 : e];
-                u[NV == 1 ? 0 : e] = fmaf(d, d, u[NV == 1 ? 0 : e]);
-            }
-#pragma unroll
-            for (int e = 0; e < NV; ++e) s[e] += i * g.P < left ? u[e] : 0.f;
+            float v[8];
+            unpack8<T>(raw[i], v);
+            cf.apply(v, sp, p.act);
+            out.store(v, i, i * g.P < me.left, p.nt);
         }
-    sum(s, gi);
-    // (columns of vectors past the chunk are of no group)
-    float *const mine = TILES ? p.part + ((image * g.tiles + at.tile) * p.G + at.chunk * g.ng) * 2
-                              : p.stats ? p.stats + (image * p.G + at.chunk * g.ng) * 2 : nullptr;
-    // One thread of each group's first channels has what its statistics are
-    if (on && prow == 0 && mine && 8 * vec < at.w)
+}
+
+// First kernel of large images: each group's (mean, M2) of a tile.  A thread takes the means of the channels it
+// holds over its pixels of a turn, then the squares about them, and joins them to those of its earlier turns (every
+// channel for itself: eight chains of sums side by side).
+template <typename T, Tail TAIL, int NV, int K>
+__global__ __launch_bounds__(1024) void gn_fwd_tiles_kernel(GroupNormArgs p)
+{
+    extern __shared__ __attribute__((aligned(16))) float lds[];
+    const Place at(p);
+    const Geo &g = p.g;
+    const Thread me(p, at);
+    const Part<T, TAIL> in(p.x, me.first, me.prow, p.C, g.P, me.vec, at.w);
+    float mean[8] = {}, m2[8] = {}, n = 0.f;
+    Raw8<T> one[K], two[K];
+    auto fetch = [&](Raw8<T>(&raw)[K], int i0) __attribute__((always_inline)) {
 #pragma unroll
-        for (int e = 0; e < NV; ++e) {
-            const int c = 8 * vec + e;
-            if (c < at.w && c % p.cpg == 0)
-                *(f32x2 *)(mine + 2 * gi[e]) = TILES ? f32x2{cf.mean[e], s[e]} : f32x2{cf.mean[e], 1.f / sqrtf(s[e] / count + p.eps)};
+        for (int i = 0; i < K; ++i) in.load(raw[i], i0 + i, (i0 + i) * g.P < me.left && i0 + i < g.k);
+    };
+    auto add = [&](Raw8<T>(&raw)[K], int i0) __attribute__((always_inline)) {
+        const int have = min(min(K, g.k - i0), max(0, (me.left + g.P - 1) / g.P - i0));   // of the K pixels
+        if (have <= 0) return;
+        const float now = (float)have, rn = 1.f / now, share = now / (n + now);
+        float s[8] = {}, q[8] = {};
+#pragma unroll
+        for (int i = 0; i < K; ++i) {   // (what is not there was loaded as zeros)
+            float v[8];
+            in.settle(raw[i]);
+            unpack8<T>(raw[i], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += v[e];
         }
-    if constexpr (!TILES) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) cf.a[e] *= 1.f / sqrtf(s[NV == 1 ? 0 : e] / count + p.eps);
+        for (int e = 0; e < 8; ++e) s[e] *= rn;
 #pragma unroll
         for (int i = 0; i < K; ++i)
-            if (i < g.k) {
+            if (i < have) {
                 float v[8];
-                raw[i].get(v, vec, g.V, at.w);
-                cf.apply(v, p.act);
-                if (on && i * g.P < left) Row<T, 8, TAIL>::store((char *)p.out + start + i * step, vec, g.V, at.w, v);
+                unpack8<T>(raw[i], v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float d = v[e] - s[e];
+                    q[e] = fmaf(d, d, q[e]);
+                }
             }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float d = s[e] - mean[e];
+            mean[e] = fmaf(d, share, mean[e]);
+            m2[e] += fmaf(d * d, n * share, q[e]);
+        }
+        n += now;
+    };
+    fetch(one, 0);   // one turn is on its way while the other is added
+    for (int i0 = 0; i0 < g.k; i0 += 2 * K) {
+        fetch(two, i0 + K);
+        add(one, i0);
+        fetch(one, i0 + 2 * K);
+        add(two, i0 + K);
     }
+    // Over the channels and threads: the mean of the means, then the squares about it
+    GroupSum<NV, 1> sum(p, lds, me);
+    const Split<NV> sp(me.vec, p.cpg, at.ngl);
+    const float count = (float)min((int64_t)g.P * g.k, p.pixels - (int64_t)at.tile * g.P * g.k) * (float)p.cpg;
+    float c[8], s[1][NV], all[NV];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = n > 0.f ? mean[e] * n : 0.f;   // (a thread without pixels: 0 times nothing)
+    sp.collapse(c, s[0]);
+    sum(s, sp);
+#pragma unroll
+    for (int e = 0; e < NV; ++e) all[e] = s[0][e] / count;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float d = mean[e] - sp.pick(all, e);
+        c[e] = n > 0.f && 8 * me.vec + e < at.w ? fmaf(d * d, n, m2[e]) : 0.f;
+    }
+    sp.collapse(c, s[0]);
+    sum(s, sp);
+    leave_groups<NV>(p, at, me, sp, p.part + ((me.image * p.G + at.chunk * g.ng) * g.tiles + at.tile) * 2, 2 * g.tiles, all, s[0]);
 }
 
 // Second kernel of large images: the tiles' statistics joined, then the tile's y.
@@ -115,95 +204,106 @@ template <typename T, Tail TAIL, int NV, int K>
 __global__ __launch_bounds__(1024) void gn_fwd_apply_kernel(GroupNormArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) float lds[];   // [ng][2]
-    const Place<true> at(p, gridDim.x);
+    const Place at(p);
     const Geo &g = p.g;
-    const int t = threadIdx.x, vec = t % g.V, prow = t / g.V;
-    const int64_t image = at.image, per_tile = (int64_t)g.P * g.k, first = at.tile * per_tile;
-    const int64_t rows = min(per_tile, p.pixels - first);
-    const int left = (int)(rows - prow);
-    const int64_t start = ((image * p.pixels + first + prow) * p.C + at.c0) * T::SIZE, step = (int64_t)g.P * p.C * T::SIZE;
-    Row<T, 8, TAIL> raw[K];
+    const Thread me(p, at);
+    const Part<T, TAIL> in(p.x, me.first, me.prow, p.C, g.P, me.vec, at.w), out(p.out, me.first, me.prow, p.C, g.P, me.vec, at.w);
+    Raw8<T> one[K], two[K];
+    auto fetch = [&](Raw8<T>(&raw)[K], int i0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < K; ++i)
-        if (i < g.k) raw[i].load((const char *)p.x + start + i * step, vec, g.V, at.w, i * g.P < left);
-    Coef<TAIL, NV> cf;
-    load_vec<8, TAIL>(p.w ? p.w + at.c0 : nullptr, 1.f, vec, g.V, at.w, cf.a);
-    load_vec<8, TAIL>(p.b ? p.b + at.c0 : nullptr, 0.f, vec, g.V, at.w, cf.b);
-    // A wave a group, its lanes the tiles: the mean by its distance from the first tile's, then M2
-    const int lane = t & 63, waves = blockDim.x >> 6;   // (whole ones, at least one)
-    const float last = (float)(p.pixels - (g.tiles - 1) * per_tile), all = (float)p.pixels;
+        for (int i = 0; i < K; ++i) in.load(raw[i], i0 + i, (i0 + i) * g.P < me.left && i0 + i < g.k);
+    };
+    fetch(one, 0);
+    Coef<NV> cf;
+    load_vec<8, TAIL>(p.w ? p.w + at.c0 : nullptr, 1.f, me.vec, g.V, at.w, cf.a);
+    load_vec<8, TAIL>(p.b ? p.b + at.c0 : nullptr, 0.f, me.vec, g.V, at.w, cf.b);
+    // A wave a group, its lanes the tiles (asked for once, where 64 hold them): the mean by its distance from the
+    // first tile's, then M2
+    const int t = threadIdx.x, lane = t & 63, waves = blockDim.x >> 6;   // (whole ones, at least one)
+    const int64_t per_tile = (int64_t)g.P * g.k;
+    const float all = (float)p.pixels, each = (float)per_tile, last = (float)(p.pixels - (g.tiles - 1) * per_tile);
     if (t >> 6 < waves)
         for (int j = t >> 6; j < at.ngl; j += waves) {
-            const float *part = p.part + (image * g.tiles * p.G + at.chunk * g.ng + j) * 2;
-            const float m0 = part[0];
+            const f32x2 *part = (const f32x2 *)p.part + (me.image * p.G + at.chunk * g.ng + j) * g.tiles;
+            const f32x2 own = part[min(lane, g.tiles - 1)];
+            const float m0 = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(own[0])));
             float d = 0.f, m2 = 0.f;
             for (int i = lane; i < g.tiles; i += 64)
-                d = fmaf((i + 1 < g.tiles ? (float)per_tile : last) / all, part[(int64_t)i * p.G * 2] - m0, d);
+                d = fmaf((i + 1 < g.tiles ? each : last) / all, (i == lane ? own[0] : part[i][0]) - m0, d);
             const float mean = m0 + wave_sum(d);
             for (int i = lane; i < g.tiles; i += 64) {
-                const f32x2 q = *(const f32x2 *)(part + (int64_t)i * p.G * 2);
+                const f32x2 q = i == lane ? own : part[i];
                 const float e = q[0] - mean;
-                m2 += q[1] + e * e * ((i + 1 < g.tiles ? (float)per_tile : last) * (float)p.cpg);
+                m2 += q[1] + e * e * ((i + 1 < g.tiles ? each : last) * (float)p.cpg);
             }
             const float inv = 1.f / sqrtf(wave_sum(m2) / (all * (float)p.cpg) + p.eps);
             if (lane == 0) {
                 lds[2 * j] = mean;
                 lds[2 * j + 1] = inv;
-                if (at.tile == 0 && p.stats) *(f32x2 *)(p.stats + (image * p.G + at.chunk * g.ng + j) * 2) = f32x2{mean, inv};
+                if (at.tile == 0 && p.stats) *(f32x2 *)(p.stats + (me.image * p.G + at.chunk * g.ng + j) * 2) = f32x2{mean, inv};
             }
         }
-    int gi[NV];
-    groups_of<NV>(vec, p.cpg, at.ngl, gi);
+    const Split<NV> sp(me.vec, p.cpg, at.ngl);
     __syncthreads();
+    float inv[NV];
 #pragma unroll
-    for (int e = 0; e < NV; ++e) cf.mean[e] = lds[2 * gi[e]];
+    for (int e = 0; e < NV; ++e) {
+        cf.mean[e] = lds[2 * sp.gi[e]];
+        inv[e] = lds[2 * sp.gi[e] + 1];
+    }
+    cf.set(inv, sp, p.act);
+    auto finish = [&](Raw8<T>(&raw)[K], int i0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) cf.a[e] *= lds[2 * gi[NV == 1 ? 0 : e] + 1];
-#pragma unroll
-    for (int i = 0; i < K; ++i)
-        if (i < g.k) {
+        for (int i = 0; i < K; ++i) {
             float v[8];
-            raw[i].get(v, vec, g.V, at.w);
-            cf.apply(v, p.act);
-            if (i * g.P < left) Row<T, 8, TAIL>::store((char *)p.out + start + i * step, vec, g.V, at.w, v);
+            in.settle(raw[i]);
+            unpack8<T>(raw[i], v);
+            cf.apply(v, sp, p.act);
+            out.store(v, i0 + i, (i0 + i) * g.P < me.left && i0 + i < g.k, p.nt);
         }
+    };
+    for (int i0 = 0; i0 < g.k; i0 += 2 * K) {
+        fetch(two, i0 + K);
+        finish(one, i0);
+        fetch(one, i0 + 2 * K);
+        finish(two, i0 + K);
+    }
 }
 
-template <typename T, Tail TAIL, int NV, int K>
-hipError_t launch_k(const GroupNormArgs &a, hipStream_t st)
+template <typename Kern>
+hipError_t launch_with(Kern k, const GroupNormArgs &a, int lds, hipStream_t st)
 {
     const Geo &g = a.g;
     const uint32_t grid = (uint32_t)((a.images + g.ipw - 1) / g.ipw * g.tiles * g.chunks);
-    const int lds = lds_floats(g, NV, 1) * (int)sizeof(float), threads = g.V * g.P * g.ipw;
-    if (g.tiles == 1) {
-        auto k = gn_fwd_kernel<T, TAIL, NV, K, false>;
-        const hipError_t e = raise_lds_limit((const void *)k, lds);
-        if (e != hipSuccess) return e;
-        return launch(k, dim3(grid), dim3(threads), lds, st, nullptr, nullptr, a);
-    }
-    auto k = gn_fwd_kernel<T, TAIL, NV, K, true>;
-    hipError_t e = raise_lds_limit((const void *)k, lds);
-    if (e == hipSuccess) e = launch(k, dim3(grid), dim3(threads), lds, st, nullptr, nullptr, a);
+    const hipError_t e = raise_lds_limit((const void *)k, lds);
     if (e != hipSuccess) return e;
-    return launch(gn_fwd_apply_kernel<T, TAIL, NV, K>, dim3(grid), dim3(threads), 2 * g.ng * (int)sizeof(float), st, nullptr, nullptr, a);
+    return launch(k, dim3(grid), dim3(threads_of(g)), lds, st, nullptr, nullptr, a);
 }
 
 template <typename T, Tail TAIL, int NV>
 hipError_t launch_tail(const GroupNormArgs &a, hipStream_t st)
 {
-    constexpr int B = 4 / T::SIZE;   // (registers of a vector: 4 B' of 16-bit types, 8 of fp32)
-    if (a.g.k <= 2 * B) return launch_k<T, TAIL, NV, 2 * B>(a, st);
-    if (a.g.k <= 6 * B) return launch_k<T, TAIL, NV, 6 * B>(a, st);
-    return launch_k<T, TAIL, NV, 12 * B>(a, st);
+    constexpr int B = 4 / T::SIZE, TURN = fwd_turn(NV) * B;   // a vector takes 4 registers of 16-bit types, 8 of fp32
+    const int lds = sum_floats(a.g, NV, 1) * (int)sizeof(float), k = a.g.k;
+    if (a.g.tiles > 1) {
+        const hipError_t e = launch_with(gn_fwd_tiles_kernel<T, TAIL, NV, TURN>, a, lds, st);
+        if (e != hipSuccess) return e;
+        return launch_with(gn_fwd_apply_kernel<T, TAIL, NV, TURN>, a, 2 * a.g.ng * (int)sizeof(float), st);
+    }
+    if (k <= 2 * B) return launch_with(gn_fwd_kernel<T, TAIL, NV, 2 * B>, a, lds, st);
+    if (k <= 4 * B) return launch_with(gn_fwd_kernel<T, TAIL, NV, 4 * B>, a, lds, st);
+    if (NV < 8 && k <= 7 * B) return launch_with(gn_fwd_kernel<T, TAIL, NV, 7 * B>, a, lds, st);
+    return launch_with(gn_fwd_kernel<T, TAIL, NV, fwd_most(NV) * B>, a, lds, st);
 }
 
 template <typename T>
 hipError_t launch_type(const GroupNormArgs &a, hipStream_t st)
 {
     if (a.cpg % 8 == 0) return launch_tail<T, WHOLE, 1>(a, st);
-    if (a.C % 8 == 0 && a.g.ng * a.cpg % 8 == 0) return launch_tail<T, WHOLE, 8>(a, st);
-    if (a.C >= 8) return launch_tail<T, PART, 8>(a, st);
-    return launch_tail<T, SHORT, 8>(a, st);   // (one chunk)
+    const bool whole = a.C % 8 == 0 && (a.g.chunks == 1 || a.g.ng * a.cpg % 8 == 0);
+    if (a.cpg > 8) return whole ? launch_tail<T, WHOLE, 2>(a, st) : launch_tail<T, PART, 2>(a, st);
+    if (whole) return launch_tail<T, WHOLE, 8>(a, st);
+    return a.C >= 8 ? launch_tail<T, PART, 8>(a, st) : launch_tail<T, SHORT, 8>(a, st);   // (shorter: one chunk)
 }
 
 }  // namespace

@@ -11,7 +11,10 @@ namespace gnorm {
 Geo plan_group_norm(const cbr_group_norm_shape &s, bool backward)
 {
     const int cpg = s.channels / s.groups, size = s.type == CBR_F32 ? 4 : 2;
-    const int most = (backward ? 24 : 48) / size;   // vectors of x (and dy) a thread holds: 96 registers
+    const int nv = split_of(cpg);
+    // pixels a thread holds of images held whole
+    const int most = (backward ? bwd_most(nv) : fwd_most(nv)) * 4 / size;
+    const int64_t row = (int64_t)s.channels * size, limit = 0x7fffffff / row;   // pixels within 2^31 bytes
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     Geo best{};
     double least = 0;
@@ -36,32 +39,43 @@ Geo plan_group_norm(const cbr_group_norm_shape &s, bool backward)
             g.ng = ng;
             g.chunks = chunks;
             g.P = std::max(1, threads / V);
-            while (g.P > 1 && g.P / 2 >= s.pixels) g.P = pow2 ? g.P / 2 : (g.P + 1) / 2;
-            g.ipw = (int)std::max<int64_t>(1, std::min<int64_t>(threads / (V * g.P), s.images));
+            while (g.P > 1 && (g.P / 2 >= s.pixels || g.P > limit)) g.P = pow2 ? g.P / 2 : (g.P + 1) / 2;
+            g.ipw = (int)std::max<int64_t>(1, std::min<int64_t>({threads / (V * g.P), s.images, limit / s.pixels}));
             const int64_t k = up(s.pixels, g.P);
-            if (k <= most) {
+            if (k <= most && g.ipw * s.pixels <= limit) {
                 g.tiles = 1;
                 g.k = (int)k;
             } else {
+                // tiles for two workgroups a CU, of 64 pixels a thread at most
                 g.ipw = 1;
-                if (V * g.P < 64 || threads < 512) continue;   // (fewer and larger tiles)
-                const int64_t per = std::min<int64_t>(k, most / 2);
-                g.tiles = (int)up(s.pixels, g.P * per);
-                g.k = (int)up(s.pixels, (int64_t)g.tiles * g.P);
+                if (V * g.P < 64 || threads < 512) continue;
+                const int64_t per = std::min(std::min<int64_t>(k, 64), std::max<int64_t>(1, limit / g.P));
+                const int64_t tiles = std::max<int64_t>({2, up(s.pixels, g.P * per), std::min<int64_t>(k, up(512, s.images * chunks))});
+                g.k = (int)up(s.pixels, tiles * g.P);
                 g.tiles = (int)up(s.pixels, (int64_t)g.P * g.k);
+                if (g.tiles < 2) continue;
             }
             g.pre = pow2 && V <= 64 && V * g.P % 64 == 0;
-            if (lds_floats(g, cpg % 8 || backward ? 8 : 1, backward ? 2 : 1) > 40 * 1024) continue;   // of a CU's 160 KB
-            const double wgs = (double)up(s.images, g.ipw) * g.tiles * chunks;
-            const int t = g.V * g.P * g.ipw, share = std::max(1, (g.k > most / 2 ? 1024 : 2048) / std::max(t, 64));
-            const double bytes = (double)g.ipw * std::min<int64_t>(s.pixels, (int64_t)g.P * g.k) * ng * cpg * size * (backward ? 3 : 2);
-            const double width = (double)ng * cpg * size, narrow = width >= 128 ? 1. : width >= 64 ? 1.1 : width >= 32 ? 1.3 : 2.;   // of cache lines
-            const double at_once = std::min(wgs, 256. * share), per_cu = std::max(1., at_once / 256.);
-            const double rate = std::min(60e3, 5.0e6 / std::min(wgs, 256.));   // bytes a us and CU
-            const double rounds = std::max(1., wgs / (256. * share));
-            double time = 3. + rounds * (1.5 + per_cu * bytes * narrow / rate) + (g.pre ? 0. : 0.5);
+            if ((backward ? bwd_floats(g, cpg) : sum_floats(g, nv, 1)) > 40 * 1024) continue;   // floats: a CU's 160 KB
+            // Expected time in us, fitted to measurements: 5 TB/s over all CUs and 60 GB/s for one; runs of a pixel's
+            // channels shorter than 64 bytes cost; a workgroup that has its CU to itself (by its registers) loads, sums
+            // and stores one after the other; SiLU's gradient is half as much arithmetic as loads and stores.
+            const int t = V * g.P * g.ipw, f = 4 / size;
+            const int waves = backward ? (g.k <= f ? 24 : g.k <= 2 * f ? 20 : 16) : g.k <= 2 * f ? 32 : g.k <= 4 * f ? 24 : 16;
+            const int share = std::max(1, waves * 64 / std::max(t, 64));
+            const double wgs = (double)up(s.images, g.ipw) * g.tiles * chunks, at_once = std::min(wgs, 256. * share);
+            const double width = (double)ng * cpg * size, narrow = width >= 64 ? 1. : width >= 32 ? 1.2 : 1.6;
+            const double values = (double)g.ipw * std::min<int64_t>(s.pixels, (int64_t)g.P * g.k) * ng * cpg;
+            const double per_cu = std::max(1., at_once / 256.), rate = std::min(60e3, 5.0e6 / std::min(wgs, 256.));
+            double one = per_cu * values * size * (backward ? 3 : 2) * narrow / rate;
+            if (g.tiles > 1) {
+                one *= backward ? 5. / 3. : 1.5;
+            } else {
+                if (share == 1) one *= 1.3;
+                one += per_cu * values * (s.act == CBR_ACT_SILU ? (backward ? 0.35 : 0.1) : 0.05) / 4000.;
+            }
+            double time = (g.tiles > 1 ? 9. : 4.) + std::max(1., wgs / (256. * share)) * (1. + one) + (g.pre ? 0. : 1.);
             if (loose) time *= 1.1;
-            if (g.tiles > 1) time = 4. + time * (backward ? 1.67 : 1.5);
             if (least == 0 || time < least) {
                 least = time;
                 best = g;

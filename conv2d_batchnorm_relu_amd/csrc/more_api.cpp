@@ -34,7 +34,7 @@ int check_group_norm(const cbr_group_norm_shape *s, bool backward, gnorm::Geo &g
     if (!float_type(s->type) || (s->act != CBR_ACT_NONE && s->act != CBR_ACT_RELU && s->act != CBR_ACT_SILU) || !(s->eps >= 0.f) ||
         !isfinite(s->eps))
         return CBR_E_VALUE;
-    if (s->images > MAX_ROWS || s->pixels > MAX_ROWS || s->channels / s->groups > MAX_GROUP) return CBR_E_UNSUPPORTED;
+    if (s->images > MAX_ROWS || s->pixels > MAX_ROWS || s->channels / s->groups > MAX_GROUP || s->channels >= 1 << 24) return CBR_E_UNSUPPORTED;
     // within 2^46 values nothing below overflows; a launch holds fewer than 2^32 threads
     if ((double)s->images * (double)s->pixels * s->channels > 0x1p46) return CBR_E_UNSUPPORTED;
     g = gnorm::plan_group_norm(*s, backward);
@@ -79,6 +79,7 @@ gnorm::GroupNormArgs norm_args(const cbr_group_norm_shape *s, const gnorm::Geo &
 {
     gnorm::GroupNormArgs a{};
     a.g = g;
+    a.nt = gnorm::streams(*s, g);
     a.images = s->images;
     a.pixels = s->pixels;
     a.C = s->channels;

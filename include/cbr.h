@@ -372,7 +372,7 @@ int cbr_gemm_fp8(const cbr_gemm_shape *shape, const void *a, const float *a_scal
  * x, y, dx, dy have `type` (CBR_BF16, CBR_F16 or CBR_F32); w, b, their gradients and the
  * statistics are float.  Everything is computed in fp32 and rounded once.
  *
- * Limits: channels a multiple of groups (CBR_E_SHAPE); channels / groups <= 8192, images and
+ * Limits: channels a multiple of groups (CBR_E_SHAPE); channels / groups <= 8192, channels < 2^24, images and
  * pixels < 2^31, at most 2^46 values, and not so many small groups or images that a launch
  * would need 2^32 threads (CBR_E_UNSUPPORTED): 2^31 values are always fewer.
  */

@@ -7,14 +7,50 @@
 
 namespace cbr {
 namespace gnorm {
+namespace {
+
+// Expected time of a layout in us, fitted to some 5000 measurements (60 shapes, up to 55 layouts each; the layout it
+// picks takes 5% longer than the fastest one in the mean, 1.3 times as long at worst).  Workgroups run in rounds of as
+// many as the registers let share the CUs; in a round a CU's loads and stores and its arithmetic overlap only in part, and
+// a workgroup alone on its CU loads, sums and stores one after the other.
+double expected_us(const cbr_group_norm_shape &s, const Geo &g, bool backward, int cpg, int nv, int size)
+{
+    auto up = [](double a, double b) { return (double)(int64_t)((a + b - 1) / b); };
+    const int f = 4 / size, t = threads_of(g);
+    const bool tiled = g.tiles > 1;
+    const int waves = tiled ? 16 : backward ? (g.k <= f ? 24 : g.k <= 2 * f ? 20 : 16) : g.k <= 2 * f ? 32 : g.k <= 4 * f ? 24 : 16;
+    const double share = std::max(1, waves * 64 / std::max(t, 64)), wgs = (double)workgroups(s, g);
+    const double act = std::min(share, up(wgs, 256.)), waves_of = up(t, 64.);
+    const double values = (double)g.ipw * std::min<int64_t>(s.pixels, (int64_t)g.P * g.k) * g.ng * cpg;
+    // memory: bytes over what a CU gets, 71 GB/s or its share of 5 TB/s, and what its loads in flight carry
+    const double width = (double)g.ng * cpg * size;
+    const bool large = (double)s.images * s.pixels * s.channels * size > 32e6;   // past the L2s: runs of a part of a line cost more
+    const double narrow = width >= 128 ? 1. : width >= 64 ? (large ? 1.05 : 1.02) : width >= 32 ? (large ? 1.35 : 1.14) : large ? 1.7 : 1.26;
+    const double passes = tiled ? (backward ? 5. : 3.) : backward ? 3. : 2.;
+    const double turn = (backward ? 2 * bwd_turn(nv) : fwd_turn(nv)) * f, held = g.k * (backward ? 2. : 1.);
+    const double flying = t * act * std::min(held, tiled ? 1.5 * turn : held) * 8 * size / 1.32;
+    const double rate = std::min(std::min(71e3, flying), 5.0e6 / std::min(wgs, 256.));
+    const double mem = act * values * size * passes * narrow / rate;
+    // arithmetic: instructions a value and pass
+    const double ins = (s.act == CBR_ACT_SILU ? (backward ? 37. : 19.7) : backward ? 13. : 9.) * (nv > 1 ? 5.5 : 1.);
+    const double alu = std::max(1., waves_of * act / 4.) * g.k * ins * 0.0057;
+    // the sums over a workgroup, and what the second kernel of large images reads before it begins
+    const double sums = 0.19 * (tiled ? 2 : 1) * (g.pre ? 1 : 2) * up(t, 256.);
+    const double join = !tiled ? 0. : 0.38 * up(g.tiles, 64.) * (backward ? up(g.V * 128., t) : up(g.ng, std::max(t / 64, 1)));
+    const double rounds = std::max(1., wgs / (256. * share)), whole = rounds < 6. ? 0.18 * up(wgs, 256. * share) + 0.82 * rounds : rounds;
+    double one = 1.5 + sums + join + std::max(mem, alu) + (tiled ? 0.1 : 2.4) * std::min(mem, alu);
+    if (!tiled && act == 1. && rounds > 1.) one += 0.16 * mem;
+    if (tiled && large && t < 512) one *= 1.08;   // (fewer waves to a CU)
+    return 2.3 + (tiled ? 4.6 : 0.) + (backward && s.images * g.tiles > 1 ? 3.1 : 0.) + whole * one;
+}
+
+}  // namespace
 
 Geo plan_group_norm(const cbr_group_norm_shape &s, bool backward)
 {
-    const int cpg = s.channels / s.groups, size = s.type == CBR_F32 ? 4 : 2;
-    const int nv = split_of(cpg);
-    // pixels a thread holds of images held whole
-    const int most = (backward ? bwd_most(nv) : fwd_most(nv)) * 4 / size;
-    const int64_t row = (int64_t)s.channels * size, limit = 0x7fffffff / row;   // pixels within 2^31 bytes
+    const int cpg = s.channels / s.groups, size = s.type == CBR_F32 ? 4 : 2, nv = split_of(cpg);
+    const int most = (backward ? bwd_most(nv) : fwd_most(nv)) * 4 / size;   // pixels a thread holds of images held whole
+    const int64_t limit = 0x7fffffff / ((int64_t)s.channels * size);        // pixels within 2^31 bytes
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     Geo best{};
     double least = 0;
@@ -30,7 +66,6 @@ Geo plan_group_norm(const cbr_group_norm_shape &s, bool backward)
         const int V = (int)up((int64_t)ng * cpg, 8), chunks = (int)up(s.groups, ng);
         if (V > 1024 || (least > 0 && (int64_t)ng * cpg * size > 1024 && s.pixels > 8)) break;
         if (!fits(ng)) continue;
-        const bool all = ng == s.groups, loose = cpg % 8 && ((int64_t)ng * cpg % 8 || s.channels % 8);
         const bool pow2 = (V & (V - 1)) == 0;
         for (int threads = 64; threads <= 1024; threads *= 2) {
             if (threads < V && threads < 1024) continue;
@@ -40,48 +75,33 @@ Geo plan_group_norm(const cbr_group_norm_shape &s, bool backward)
             g.chunks = chunks;
             g.P = std::max(1, threads / V);
             while (g.P > 1 && (g.P / 2 >= s.pixels || g.P > limit)) g.P = pow2 ? g.P / 2 : (g.P + 1) / 2;
-            g.ipw = (int)std::max<int64_t>(1, std::min<int64_t>({threads / (V * g.P), s.images, limit / s.pixels}));
+            g.pre = pow2 && V <= 64 && V * g.P % 64 == 0;
+            auto weigh = [&]() {
+                if ((backward ? bwd_floats(g, cpg) : sum_floats(g, nv, 1)) > 40 * 1024) return;   // floats: a CU's 160 KB
+                const double time = expected_us(s, g, backward, cpg, nv, size);
+                if (least == 0 || time < least) {
+                    least = time;
+                    best = g;
+                }
+            };
             const int64_t k = up(s.pixels, g.P);
+            g.ipw = (int)std::max<int64_t>(1, std::min<int64_t>({threads / (V * g.P), s.images, limit / s.pixels}));
             if (k <= most && g.ipw * s.pixels <= limit) {
                 g.tiles = 1;
                 g.k = (int)k;
-            } else {
-                // tiles for two workgroups a CU, of 64 pixels a thread at most
-                g.ipw = 1;
-                if (V * g.P < 64 || threads < 512) continue;
-                const int64_t per = std::min(std::min<int64_t>(k, 64), std::max<int64_t>(1, limit / g.P));
-                const int64_t tiles = std::max<int64_t>({2, up(s.pixels, g.P * per), std::min<int64_t>(k, up(512, s.images * chunks))});
+                weigh();
+            }
+            // tiles for one, two or four workgroups a CU (a small call is not worth a second kernel, nor weighing it)
+            g.ipw = 1;
+            if (V * g.P < 64 || threads < 256 || k < 2 || (least > 0 && (double)s.images * s.pixels * s.channels < 250e3)) continue;
+            for (int64_t total = 256; total <= 1024; total *= 2) {
+                const int64_t tiles = std::max<int64_t>({2, up(s.pixels, g.P * std::max<int64_t>(1, limit / g.P)), std::min<int64_t>(k, total / (s.images * chunks))});
                 g.k = (int)up(s.pixels, tiles * g.P);
                 g.tiles = (int)up(s.pixels, (int64_t)g.P * g.k);
-                if (g.tiles < 2) continue;
-            }
-            g.pre = pow2 && V <= 64 && V * g.P % 64 == 0;
-            if ((backward ? bwd_floats(g, cpg) : sum_floats(g, nv, 1)) > 40 * 1024) continue;   // floats: a CU's 160 KB
-            // Expected time in us, fitted to measurements: 5 TB/s over all CUs and 60 GB/s for one; runs of a pixel's
-            // channels shorter than 64 bytes cost; a workgroup that has its CU to itself (by its registers) loads, sums
-            // and stores one after the other; SiLU's gradient is half as much arithmetic as loads and stores.
-            const int t = V * g.P * g.ipw, f = 4 / size;
-            const int waves = backward ? (g.k <= f ? 24 : g.k <= 2 * f ? 20 : 16) : g.k <= 2 * f ? 32 : g.k <= 4 * f ? 24 : 16;
-            const int share = std::max(1, waves * 64 / std::max(t, 64));
-            const double wgs = (double)up(s.images, g.ipw) * g.tiles * chunks, at_once = std::min(wgs, 256. * share);
-            const double width = (double)ng * cpg * size, narrow = width >= 64 ? 1. : width >= 32 ? 1.2 : 1.6;
-            const double values = (double)g.ipw * std::min<int64_t>(s.pixels, (int64_t)g.P * g.k) * ng * cpg;
-            const double per_cu = std::max(1., at_once / 256.), rate = std::min(60e3, 5.0e6 / std::min(wgs, 256.));
-            double one = per_cu * values * size * (backward ? 3 : 2) * narrow / rate;
-            if (g.tiles > 1) {
-                one *= backward ? 5. / 3. : 1.5;
-            } else {
-                if (share == 1) one *= 1.3;
-                one += per_cu * values * (s.act == CBR_ACT_SILU ? (backward ? 0.35 : 0.1) : 0.05) / 4000.;
-            }
-            double time = (g.tiles > 1 ? 9. : 4.) + std::max(1., wgs / (256. * share)) * (1. + one) + (g.pre ? 0. : 1.);
-            if (loose) time *= 1.1;
-            if (least == 0 || time < least) {
-                least = time;
-                best = g;
+                if (g.tiles > 1) weigh();
             }
         }
-        if (all) break;
+        if (ng == s.groups) break;
     }
     return best;
 }

@@ -53,7 +53,7 @@ __device__ __forceinline__ uint32_t lds_read2(uint32_t addr)
 // Tile kernel: 16 MS WM x 16 NS WN results a workgroup, WM x WN waves of 16 MS x 16 NS.  Both operands'
 // rows of a stage and their exponents come straight into LDS, NST stages deep, as in the 8-bit product.
 template <int BM, int BN>
-constexpr int word_row() { return (BM + BN) * 4 + 64; }   // words of a stage's half, sixteen banks apart
+constexpr int word_row() { return (BM + BN) * 4 + 128; }   // words of a stage's half, 32 banks apart
 template <int BM, int BN>
 constexpr int stage_bytes() { return (BM + BN) * BK + 2 * word_row<BM, BN>(); }
 
@@ -62,10 +62,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm4_tile_kernel(Fp4Args p)
 {
     constexpr int NW = WM * WN, BM = 16 * MS * WM, BN = 16 * NS * WN;
     constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;        // load instructions a wave, 8 rows each
-    constexpr int LS = (BM + BN) / 64 * 2;                   // of exponents, 64 rows each, for all waves
-    constexpr int PER = LA + LB + (LS + NW - 1) / NW;
+    constexpr int LS = (BM + BN) / 64 * 2 / NW;              // of exponents, 64 rows each: of a half the waves, of b the others
+    constexpr int PER = LA + LB + LS;
     constexpr int STAGE = stage_bytes<BM, BN>(), WORDS = (BM + BN) * BK, HALF = word_row<BM, BN>();
-    static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN && LS % NW == 0, "tile shape");
+    static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN && BM == BN && LS * 64 * NW == 2 * (BM + BN), "tile shape");
     static_assert(NS % 2 == 0 && MS >= 2, "products in pairs, loads at the second fragment");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const uint32_t lbase = (uint32_t)(uintptr_t)(lds_u8 *)lds;
@@ -87,25 +87,29 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm4_tile_kernel(Fp4Args p)
                                                                         (int)((uint32_t)rows_b * p.ldb), 0x00020000);
     const int lrow = 8 * wave + (lane >> 3);
     const int lchunk = 16 * ((lane & 7) ^ perm(lrow)), lchunk_b = 16 * ((lane & 7) ^ perm_b<F32>(lrow));
-    auto load = [&](int t, int st) __attribute__((always_inline)) {
+    // (scalars of the wave: taken by value below, where a choice between captured ones would go through memory)
+    const bool of_a = wave < NW / 2;
+    const int first = of_a ? wave : wave - NW / 2, s_lds = of_a ? 0 : BM * 4;
+    const int s_len = 4 * (of_a ? rows_a : rows_b);
+    const int64_t s_ld = of_a ? p.M : (int64_t)p.N;
+    const uint32_t *const s_from = of_a ? p.sa + m0 : p.sb + n0;
+    auto load = [=](int t, int st) __attribute__((always_inline)) {
         const int kat = t * BK + lchunk, kbt = t * BK + lchunk_b;   // groups past the end: zeros
         lds_u8 *base = (lds_u8 *)lds + st * STAGE;
         lds_u8 *dst = base + wave * 1024;
+        const int va = kat < p.bytes ? lrow * p.lda + kat : (int)OOB, vb = kbt < p.bytes ? lrow * p.ldb + kbt : (int)OOB;
 #pragma unroll
         for (int i = 0; i < LA; ++i)
-            buffer_load_lds16(ra, dst + i * NW * 1024, kat < p.bytes ? (lrow + i * 8 * NW) * p.lda + kat : (int)OOB);
+            buffer_load_lds16(ra, dst + i * NW * 1024, va + i * 8 * NW * p.lda);   // (OOB and 2^30 more stays past the end)
 #pragma unroll
         for (int i = 0; i < LB; ++i)
-            buffer_load_lds16(rb, dst + BM * BK + i * NW * 1024, kbt < p.bytes ? (lrow + i * 8 * NW) * p.ldb + kbt : (int)OOB);
+            buffer_load_lds16(rb, dst + BM * BK + i * NW * 1024, vb + i * 8 * NW * p.ldb);
 #pragma unroll
-        for (int i = 0; i < LS / NW; ++i) {
-            // 64 words: of half h, of rows at .. at + 63 of a and then b
-            const int n = i * NW + wave, h = n / (LS / 2), at = n % (LS / 2) * 64, word = 2 * t + h;
-            const bool of_a = at < BM;
-            const uint32_t *from = of_a ? p.sa + (int64_t)word * p.M + m0 : p.sb + (int64_t)word * p.N + n0;
+        for (int i = 0; i < LS; ++i) {   // half h's words of 64 rows
+            const int n = i * (NW / 2) + first, h = n / (BM / 64), at = n % (BM / 64) * 64, word = 2 * t + h;
             const __amdgpu_buffer_rsrc_t rs =
-                __builtin_amdgcn_make_buffer_rsrc((void *)from, 0, word < p.words ? 4 * (of_a ? rows_a : rows_b) : 0, 0x00020000);
-            buffer_load_lds4(rs, base + WORDS + h * HALF + at * 4, ((of_a ? at : at - BM) + lane) * 4);
+                __builtin_amdgcn_make_buffer_rsrc((void *)(s_from + word * s_ld), 0, word < p.words ? s_len : 0, 0x00020000);
+            buffer_load_lds4(rs, base + WORDS + h * HALF + s_lds + at * 4, (at + lane) * 4);
         }
     };
 

@@ -42,11 +42,13 @@ __device__ __forceinline__ f32x4 product(u32x4 b, u32x4 a, f32x4 c, uint32_t sb,
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, S, (int)sb, S, (int)sa);
 }
 
+// A word of exponents.  (Each lane group its own two bytes, read as such: 8 cycles of conflicts a read, as much as all
+// fragments take.)
 template <int OFF>
-__device__ __forceinline__ uint32_t lds_read2(uint32_t addr)
+__device__ __forceinline__ uint32_t lds_word(uint32_t addr)
 {
     uint32_t v;
-    asm volatile("ds_read_u16 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFF) : "memory");
+    asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFF) : "memory");
     return v;
 }
 
@@ -122,8 +124,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm4_tile_kernel(Fp4Args p)
     const uint32_t fa0 = lbase + (wm * 16 * MS + r16) * BK + 16 * (2 * g ^ perm(r16));
     const int brow = col_in_wave<F32>(0, r16 >> 2, r16 & 3);
     const uint32_t fb0 = lbase + (BM + wn * 16 * NS + brow) * BK + 16 * (2 * g ^ perm_b<F32>(brow));
-    const uint32_t sa0 = lbase + WORDS + (g >> 1) * HALF + (wm * 16 * MS + r16) * 4 + 2 * (g & 1);
-    const uint32_t sb0 = lbase + WORDS + (g >> 1) * HALF + (BM + wn * 16 * NS + brow) * 4 + 2 * (g & 1);
+    // exponents: the word with the lane's two groups, moved to its low bytes
+    const uint32_t sa0 = lbase + WORDS + (g >> 1) * HALF + (wm * 16 * MS + r16) * 4;
+    const uint32_t sb0 = lbase + WORDS + (g >> 1) * HALF + (BM + wn * 16 * NS + brow) * 4;
+    const int shift = 16 * (g & 1);
 
 #pragma unroll
     for (int t = 0; t < NST - 1; ++t)
@@ -143,53 +147,62 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm4_tile_kernel(Fp4Args p)
         }
         const uint32_t fa = fa0 + st * STAGE, fb = fb0 + st * STAGE, fax = fa ^ 16, fbx = fb ^ 16;
         const uint32_t sa = sa0 + st * STAGE, sb = sb0 + st * STAGE;
+        // Products of the first instruction's fragments, then of the second's: so few are waited for at the beginning.
+        // Turn q: fragment q % MS of a, instruction q / MS.
         uint32_t ea[MS], eb[NS];
-        u32x4 bf[NS][2], af[3][2];
+        u32x4 bf[NS][2], af[3];
+        auto read_a = [&](auto qc) __attribute__((always_inline)) {
+            constexpr int q = decltype(qc)::value;
+            if constexpr (q < 2 * MS) af[q % 3] = lds_read16<(q % MS) * 16 * BK>(q < MS ? fa : fax);
+        };
         unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
             constexpr int i = decltype(ic)::value;
-            eb[i] = lds_read2<col_in_wave<F32>(i, 0, 0) * 4>(sb);
-        });
-        unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
-            constexpr int j = decltype(jc)::value;
-            ea[j] = lds_read2<j * 64>(sa);
+            eb[i] = lds_word<col_in_wave<F32>(i, 0, 0) * 4>(sb);
         });
         unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
             constexpr int i = decltype(ic)::value;
             bf[i][0] = lds_read16<col_in_wave<F32>(i, 0, 0) * BK>(fb);
-            bf[i][1] = lds_read16<col_in_wave<F32>(i, 0, 0) * BK>(fbx);
         });
-        unrolled<2>([&](auto jc) __attribute__((always_inline)) {
-            constexpr int j = decltype(jc)::value;
-            af[j][0] = lds_read16<j * 16 * BK>(fa);
-            af[j][1] = lds_read16<j * 16 * BK>(fax);
-        });
-        lgkm_wait<2>();   // all but the second fragment of a
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            after_wait(eb[i]);
-            after_wait(bf[i][0]);
-            after_wait(bf[i][1]);
-        }
-#pragma unroll
-        for (int j = 0; j < MS; ++j) after_wait(ea[j]);
         unrolled<MS>([&](auto jc) __attribute__((always_inline)) {
-            constexpr int J = decltype(jc)::value;
-            if constexpr (J > 0) lgkm_wait<(J + 1 < MS ? 2 : 0)>();   // all but the next fragment of a
-            after_wait(af[J % 3][0]);
-            after_wait(af[J % 3][1]);
+            constexpr int j = decltype(jc)::value;
+            ea[j] = lds_word<j * 64>(sa);
+        });
+        read_a(std::integral_constant<int, 0>{});
+        read_a(std::integral_constant<int, 1>{});
+        unrolled<2 * MS>([&](auto qc) __attribute__((always_inline)) {
+            constexpr int q = decltype(qc)::value, J = q % MS, K = q / MS;
+            // all but what was read after this fragment: the next one, and b's second ones behind turn 0
+            lgkm_wait<(q == 1 ? NS + 1 : q == 2 * MS - 1 ? 0 : 1)>();
+            if constexpr (q == 0) {
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    after_wait(eb[i]);
+                    after_wait(bf[i][0]);
+                    eb[i] >>= shift;
+                }
+#pragma unroll
+                for (int j = 0; j < MS; ++j) {
+                    after_wait(ea[j]);
+                    ea[j] >>= shift;
+                }
+            }
+            if constexpr (q == MS)
+#pragma unroll
+                for (int i = 0; i < NS; ++i) after_wait(bf[i][1]);
+            after_wait(af[q % 3]);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < NS; ++i) acc[i][J] = product<0>(bf[i][0], af[J % 3][0], acc[i][J], eb[i], ea[J]);
+            for (int i = 0; i < NS; ++i) acc[i][J] = product<K>(bf[i][K], af[q % 3], acc[i][J], eb[i], ea[J]);
+            if constexpr (q == 0)
+                unrolled<NS>([&](auto ic) __attribute__((always_inline)) {
+                    constexpr int i = decltype(ic)::value;
+                    bf[i][1] = lds_read16<col_in_wave<F32>(i, 0, 0) * BK>(fbx);
+                });
             // the next fragment but one, once the products that read its registers are under way
-            if constexpr (J + 2 < MS) {
-                af[(J + 2) % 3][0] = lds_read16<(J + 2) * 16 * BK>(fa);
-                af[(J + 2) % 3][1] = lds_read16<(J + 2) * 16 * BK>(fax);
-            }
+            read_a(std::integral_constant<int, q + 2>{});
             // Stage t + NST - 1 takes the place of stage t - 1, which every wave has read
-            if constexpr (J == 1)
+            if constexpr (q == 1)
                 if (t + NST - 1 < turns) load(t0 + t + NST - 1, st == 0 ? NST - 1 : st - 1);
-#pragma unroll
-            for (int i = 0; i < NS; ++i) acc[i][J] = product<1>(bf[i][1], af[J % 3][1], acc[i][J], eb[i], ea[J]);
             __builtin_amdgcn_sched_barrier(0);
         });
         st = st + 1 == NST ? 0 : st + 1;

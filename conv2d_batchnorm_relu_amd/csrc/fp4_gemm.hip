@@ -301,49 +301,47 @@ struct Fp4Plan {
     int splits, per, stages;
 };
 
-// The tile and the number of splits with the least expected time, in us: a stage of 256 values takes
-// `one` with one workgroup on a CU and `two` with two, a workgroup's start and end `ends`; joining splits
-// takes 4 us and moves each part twice at 4 TB/s.
+// The form and the number of splits with the least expected time, in us, fitted to measurements of 90 shapes, each in
+// all forms and with up to 13 numbers of splits: the pick takes 3% longer than the fastest in the mean, 1.2 times as
+// long at worst.  Tiles: a stage of 256 values takes `one` with one workgroup on a CU and `two` with two, a
+// workgroup's start and end `ends`.  Few rows: 1.2 and for each run 0.09 + 0.011 m (the more rows, the more loads), or
+// b at 4.3 TB/s; two workgroups share a CU up to 16 rows.  Joining splits takes 3 to 4 us and moves each part twice at
+// 4 TB/s.  (1 x 1000 x 2048: few rows 3.3 us, tiles of 64 5.8; 1 x 50000 x 512: 8.1, 6.0; 64 x 256 x 50176: 73 whole,
+// 14.4 in 16 splits, tiles of 64 in 48 splits 10.2.)
 struct Costs {
     double one, two, ends;
 };
 
 Fp4Plan plan_of(const cbr_gemm_fp4_shape &s)
 {
-    const int64_t bytes = (s.k + 31) / 32 * 16, stages = (bytes + BK - 1) / BK;
+    const int64_t bytes = (s.k + 31) / 32 * 16;
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     Fp4Plan best{};
     double least = 0;
+    auto weigh = [&](Form form, int64_t edge_m, int64_t edge_n, int64_t stages, int64_t fit, auto time) {
+        const int64_t tiles = up(s.m, edge_m) * up(s.n, edge_n), most = tiles < fit ? std::min(fit / tiles, stages) : 1;
+        for (int64_t want = 1; want <= most; want += want < 8 ? 1 : 8) {   // see place() for eights
+            const int64_t per = up(stages, want), splits = up(stages, per);
+            const double join = splits > 1 ? (form == FEW ? 3. : 3.5) + 0.03 * splits + (double)splits * s.m * s.n * 8. / 4e6 : 0.;
+            const double t = time(per, tiles * splits) + join;
+            if (best.splits == 0 || t < least) {
+                least = t;
+                best = Fp4Plan{form, (int)edge_m / 16, (int)edge_m, (int)edge_n, (int)splits, (int)per, (int)stages};
+            }
+        }
+    };
     if (s.m <= 64) {
-        best.form = FEW;
-        best.ms = s.m <= 16 ? 1 : s.m <= 32 ? 2 : 4;
-        best.bm = 16 * best.ms;
-        best.bn = 16;
-        best.stages = (int)up(bytes, RUN);
-        const int64_t tiles = up(s.n, 16);
-        const int64_t splits = tiles < 256 ? std::max<int64_t>(1, std::min<int64_t>(256 / tiles, best.stages / (2 * SKW))) : 1;
-        best.per = (int)up(best.stages, splits);
-        best.splits = (int)up(best.stages, best.per);
-        least = 2. + (double)s.n * bytes / 5.e6 * (1. + 0.032 * s.m) + (best.splits > 1 ? 3. : 0.);
+        const int64_t rows = s.m <= 16 ? 16 : s.m <= 32 ? 32 : 64;
+        weigh(FEW, rows, 16, up(bytes, RUN), 512, [&](int64_t per, int64_t wgs) {
+            return 2. + std::max(up(wgs, rows == 16 ? 512 : 256) * (1.2 + per * (0.09 + 0.011 * s.m)), s.n * bytes / 4.3e6 * (1. + 0.02 * s.m));
+        });
     }
     for (const Form form : {TILE64, TILE128, TILE256}) {
         const Costs c = form == TILE256 ? Costs{1.0, 0., 5.} : form == TILE128 ? Costs{0.5, 0.7, 3.} : Costs{0.3, 0.35, 1.6};
-        const int64_t edge = form == TILE256 ? 256 : form == TILE128 ? 128 : 64, tiles = up(s.m, edge) * up(s.n, edge);
-        const int64_t fit = form == TILE256 ? 256 : 512, most = tiles < fit ? std::min(fit / tiles, stages) : 1;
-        for (int64_t want = 1; want <= most; want += want < 8 ? 1 : 8) {   // see place() for eights
-            const int64_t per = up(stages, want), splits = up(stages, per), wgs = tiles * splits;
-            const double t = 2.3 + (wgs <= 256 || form == TILE256 ? up(wgs, 256) * (per * c.one + c.ends)
-                                                                  : up(wgs, 512) * (per * c.two + c.ends));
-            const double join = splits > 1 ? 4. + (double)splits * s.m * s.n * 8. / 4e6 : 0.;
-            if (best.splits == 0 || t + join < least) {
-                least = t + join;
-                best.form = form;
-                best.bm = best.bn = (int)edge;
-                best.stages = (int)stages;
-                best.per = (int)per;
-                best.splits = (int)splits;
-            }
-        }
+        const int64_t edge = form == TILE256 ? 256 : form == TILE128 ? 128 : 64;
+        weigh(form, edge, edge, up(bytes, BK), form == TILE256 ? 256 : 512, [&](int64_t per, int64_t wgs) {
+            return 2.3 + (wgs <= 256 || form == TILE256 ? up(wgs, 256) * (per * c.one + c.ends) : up(wgs, 512) * (per * c.two + c.ends));
+        });
     }
     return best;
 }

@@ -240,6 +240,20 @@ def test_product_sizes(size, out):
     check_product(m, n, k, a, b, out, bias, relu=i % 4 == 1)
 
 
+# every form on one round of workgroups and on more, whole and in splits
+FSIZES = [(1, 4260, 77), (7, 400, 18650), (25, 70, 9000), (17000, 1, 33), (1800, 40, 6266), (9001, 800, 96), (300, 7000, 1100), (1049, 81, 67300),
+          (12622, 3, 13860), (24000, 300, 64), (3004, 141, 93800)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", FSIZES, ids=str)
+def test_product_forms(size):
+    m, n, k = size
+    a, b = operand(m, k, 20, 1), operand(n, k, 21, 1)
+    for out in ("bf16", "f32"):
+        check_product(m, n, k, a, b, out, torch.randn(n, generator=gen(2), device="cuda"))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("size", PSIZES, ids=str)
 def test_product_of_whole_numbers_is_exact(size):

@@ -245,8 +245,8 @@ __host__ __device__ inline int sum_rows(const Geo &g) { return g.pre ? g.P * g.V
 __host__ __device__ inline bool few_rows(const Geo &g, int cpg) { return cpg % 8 == 0 ? sum_rows(g) * (cpg / 8) <= 32 : cpg > 8 && sum_rows(g) * (cpg / 4 + 1) <= 32; }
 
 // Sums of a group over the pixels and channels that the workgroup holds, twice (N values at once).  LDS:
-// [2][rows][wd] partial sums, [wd] columns, [ng ipw] groups, wd = NV V ipw, all N times.
-inline int sum_floats(const Geo &g, int nv, int n) { return n * ((2 * sum_rows(g) + 1) * nv * g.V * g.ipw + g.ng * g.ipw); }
+// [2][rows][wd] partial sums, [wd] columns, [ng ipw] groups, wd = NV V ipw, all N times; rounded up to 16 bytes.
+__host__ __device__ inline int sum_floats(const Geo &g, int nv, int n) { return (n * ((2 * sum_rows(g) + 1) * nv * g.V * g.ipw + g.ng * g.ipw) + 3) & ~3; }
 
 template <int NV, int N>
 struct GroupSum {

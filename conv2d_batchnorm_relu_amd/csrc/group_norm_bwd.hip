@@ -136,7 +136,7 @@ __global__ __launch_bounds__(1024) void gn_bwd_kernel(GroupNormArgs p)
     const Split<NV> sp(me.vec, p.cpg, at.ngl);
     Coef<NV> cf;
     cf.template load<TAIL>(p, at, me, sp);
-    float *const channels = lds + 2 * 2 * sum_rows(g) * NV * g.V * g.ipw + 2 * (NV * g.V * g.ipw + g.ng * g.ipw);   // behind the groups' sums
+    float *const channels = lds + sum_floats(g, NV, 2);
     float s[2][NV];
     {
         float s1[8] = {}, s0[8] = {};

@@ -9,6 +9,7 @@ the sigmoid has six more (two of its hardware functions' whole steps); the deriv
 three times that.  An output adds half a step of its type.  Sums of small whole numbers are exact in fp32, so a
 pixel left out or taken twice shows there."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -206,6 +207,28 @@ def test_whole_numbers_are_summed_exactly(size, dtype):
     assert ((st[..., 0].double() - mean).abs() <= U * mean.abs() + 3 * 8 * U).all()
     db = backward(t, st, dx=False, dw=False)[2]
     assert torch.equal(db.double(), t["dy"].double().sum((0, 1)))
+
+
+def drawn(i):
+    """Sizes over the whole range, of 4 million values at most."""
+    r = random.Random(i)
+    while True:
+        cpg, groups = (int(2 ** r.uniform(0, t)) for t in (10, 11))
+        images, pixels = (int(2 ** r.uniform(0, t)) for t in (9, 17))
+        if images * pixels * cpg * groups <= 4e6:
+            return images, pixels, cpg * groups, groups
+
+
+# (the last two: sums of 128 and 150 KB)
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", [drawn(i) for i in range(60)] + [(10, 13, 33155, 6631), (476, 2, 4470, 894)], ids=str)
+def test_drawn_sizes(size):
+    r = random.Random(str(size))
+    for dtype in ("f32", r.choice(("bf16", "f16"))):
+        t = make(*size, dtype, r.choice(list(ACT)), 17)
+        y, st = forward(t)
+        check_forward(t, y, st)
+        check_backward(t, st, *backward(t, st))
 
 
 @pytest.mark.gpu

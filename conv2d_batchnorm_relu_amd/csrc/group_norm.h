@@ -36,6 +36,7 @@ struct GroupNormArgs {
     int64_t images, pixels;
     int C, G, cpg, act;
     int nt;             // out is written as a stream
+    int front;          // workgroups before those of the images (see gn_bwd_apply_kernel)
     float eps;
     Geo g;
 };
@@ -47,7 +48,7 @@ struct Place {
     int64_t image;                 // the first one
     __device__ __forceinline__ explicit Place(const GroupNormArgs &p)
     {
-        const uint32_t id = blockIdx.x, x = id % 8, q = gridDim.x / 8, r = gridDim.x % 8;
+        const uint32_t id = blockIdx.x - p.front, all = gridDim.x - p.front, x = id % 8, q = all / 8, r = all % 8;
         uint32_t t = x * q + min(x, r) + id / 8;
         chunk = t % p.g.chunks;
         t /= p.g.chunks;

@@ -5,6 +5,8 @@
 // and over the images dw = sum S1, db = sum S0.  As in the forward a workgroup holds whole groups of
 // an image, here of x and dy, in registers, or (large images) one kernel leaves the tiles' S1, S0 and
 // a second one reads again.
+#include <algorithm>
+
 #include "block_launch.h"
 #include "group_norm.h"
 
@@ -247,16 +249,17 @@ __global__ __launch_bounds__(1024) void gn_bwd_tiles_kernel(GroupNormArgs p)
 }
 
 // dw, db of FC channels a workgroup: the images' and tiles' parts added in fp64, in a fixed order, by rows of FC
-// threads (64 channels a workgroup left one to read 2 MB: 12.9 us of 8 x 50176 x 64; 16: 5).
+// threads (64 channels a workgroup left one to read 2 MB: 12.9 us of 8 x 50176 x 64; 16: 5).  LDS: two doubles a thread.
 constexpr int FC = 16;
 
-__global__ __launch_bounds__(1024) void gn_bwd_finish_kernel(GroupNormArgs p)
+__device__ __forceinline__ void finish_channels(const GroupNormArgs &p, double *sums)
 {
-    extern __shared__ __attribute__((aligned(16))) double sums[];   // [rows of threads][FC][2]
-    const int c = blockIdx.x * FC + (threadIdx.x % FC), lane = threadIdx.x / FC, lanes = blockDim.x / FC;
+    int lanes = 1;   // rows of threads, a power of two
+    while (2 * lanes * FC <= (int)blockDim.x) lanes *= 2;
+    const int c = blockIdx.x * FC + (threadIdx.x % FC), lane = threadIdx.x / FC;
     const int64_t rows = p.images * p.g.tiles, ld = 2 * (int64_t)p.C;
     double s1 = 0., s0 = 0.;
-    if (c < p.C) {
+    if (c < p.C && lane < lanes) {
         const float *q = p.part + c;
         int64_t r = lane;
         for (; r + 7 * lanes < rows; r += 8 * lanes) {   // sixteen loads under way
@@ -279,7 +282,7 @@ __global__ __launch_bounds__(1024) void gn_bwd_finish_kernel(GroupNormArgs p)
     }
     sums[2 * threadIdx.x] = s1;
     sums[2 * threadIdx.x + 1] = s0;
-    for (int n = lanes / 2; n > 0; n /= 2) {   // (lanes: a power of two)
+    for (int n = lanes / 2; n > 0; n /= 2) {
         __syncthreads();
         if (lane < n) {
             s1 += sums[2 * (threadIdx.x + n * FC)];
@@ -294,8 +297,15 @@ __global__ __launch_bounds__(1024) void gn_bwd_finish_kernel(GroupNormArgs p)
     }
 }
 
+__global__ __launch_bounds__(1024) void gn_bwd_finish_kernel(GroupNormArgs p)
+{
+    extern __shared__ __attribute__((aligned(16))) double sums[];
+    finish_channels(p, sums);
+}
+
 // Second kernel of large images: the tiles' sums joined, then the tile's dx.  LDS (floats): [parts][2][8 V] sums of some
-// tiles, [2][8 V] columns, [2][ng] groups.
+// tiles, [2][8 V] columns, [2][ng] groups.  The first `front` workgroups add up dw and db beside it (a
+// kernel of its own behind this one took 2 to 3 us more: 64 x 56 x 56 x 256 110 us against 108, 2 x 4097 x 64 17.8, 16.1).
 inline __host__ __device__ int apply_parts(const Geo &g) { return max(1, min(g.V * g.P / (16 * g.V), 8)); }
 inline int apply_floats(const Geo &g) { return 16 * g.V * (apply_parts(g) + 1) + 2 * g.ng; }
 
@@ -303,6 +313,10 @@ template <typename T, Tail TAIL, int NV, int K>
 __global__ __launch_bounds__(1024) void gn_bwd_apply_kernel(GroupNormArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) float lds[];
+    if (blockIdx.x < (uint32_t)p.front) {
+        finish_channels(p, (double *)lds);
+        return;
+    }
     const Place at(p);
     const Geo &g = p.g;
     const Thread me(p, at);
@@ -373,7 +387,7 @@ template <typename Kern>
 hipError_t launch_with(Kern k, const GroupNormArgs &a, int lds, hipStream_t st)
 {
     const Geo &g = a.g;
-    const uint32_t grid = (uint32_t)((a.images + g.ipw - 1) / g.ipw * g.tiles * g.chunks);
+    const uint32_t grid = (uint32_t)((a.images + g.ipw - 1) / g.ipw * g.tiles * g.chunks) + a.front;
     const hipError_t e = raise_lds_limit((const void *)k, lds);
     if (e != hipSuccess) return e;
     return launch(k, dim3(grid), dim3(threads_of(g)), lds, st, nullptr, nullptr, a);
@@ -384,12 +398,16 @@ hipError_t launch_tail(const GroupNormArgs &a, hipStream_t st)
 {
     constexpr int B = 4 / T::SIZE, TURN = bwd_turn(NV) * B;
     const Geo &g = a.g;
-    const int lds = bwd_floats(g, a.cpg) * (int)sizeof(float);
+    const int lds = bwd_floats(g, a.cpg) * (int)sizeof(float), fin = a.part && (a.dw || a.db) ? (a.C + FC - 1) / FC : 0;
     hipError_t e;
     if (g.tiles > 1) {
         e = launch_with(gn_bwd_tiles_kernel<T, TAIL, NV, TURN>, a, lds, st);
-        if (e == hipSuccess && a.out)
-            e = launch_with(gn_bwd_apply_kernel<T, TAIL, NV, TURN>, a, apply_floats(g) * (int)sizeof(float), st);
+        if (e != hipSuccess) return e;
+        if (a.out) {
+            GroupNormArgs b = a;
+            b.front = fin;
+            return launch_with(gn_bwd_apply_kernel<T, TAIL, NV, TURN>, b, std::max(apply_floats(g) * (int)sizeof(float), fin ? threads_of(g) * 16 : 0), st);
+        }
     } else if (g.k <= B) {
         e = launch_with(gn_bwd_kernel<T, TAIL, NV, B>, a, lds, st);
     } else if (g.k <= 2 * B) {
@@ -397,9 +415,9 @@ hipError_t launch_tail(const GroupNormArgs &a, hipStream_t st)
     } else {
         e = launch_with(gn_bwd_kernel<T, TAIL, NV, bwd_most(NV) * B>, a, lds, st);
     }
-    if (e != hipSuccess || !a.part || !(a.dw || a.db)) return e;
+    if (e != hipSuccess || !fin) return e;
     const int n = a.images * g.tiles >= 64 ? 1024 : 256;
-    return launch(gn_bwd_finish_kernel, dim3((a.C + FC - 1) / FC), dim3(n), n * 16, st, nullptr, nullptr, a);
+    return launch(gn_bwd_finish_kernel, dim3(fin), dim3(n), n * 16, st, nullptr, nullptr, a);
 }
 
 template <typename T>

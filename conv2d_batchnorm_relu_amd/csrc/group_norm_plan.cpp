@@ -41,7 +41,7 @@ double expected_us(const cbr_group_norm_shape &s, const Geo &g, bool backward, i
     double one = 1.5 + sums + join + std::max(mem, alu) + (tiled ? 0.1 : 2.4) * std::min(mem, alu);
     if (!tiled && act == 1. && rounds > 1.) one += 0.16 * mem;
     if (tiled && large && t < 512) one *= 1.08;   // (fewer waves to a CU)
-    return 2.3 + (tiled ? 4.6 : 0.) + (backward && s.images * g.tiles > 1 ? 3.1 : 0.) + whole * one;
+    return 2.3 + (tiled ? 4.6 : 0.) + (backward && s.images * g.tiles > 1 ? (tiled ? 0.8 : 3.1) : 0.) + whole * one;
 }
 
 Geo least_time(const cbr_group_norm_shape &s, bool backward)

@@ -38,7 +38,8 @@ int check_group_norm(const cbr_group_norm_shape *s, bool backward, gnorm::Geo &g
     // within 2^46 values nothing below overflows; a launch holds fewer than 2^32 threads
     if ((double)s->images * (double)s->pixels * s->channels > 0x1p46) return CBR_E_UNSUPPORTED;
     g = gnorm::plan_group_norm(*s, backward);
-    return gnorm::workgroups(*s, g) * gnorm::threads_of(g) < (int64_t)1 << 32 ? CBR_OK : CBR_E_UNSUPPORTED;
+    // (and the workgroups of 16 channels before those of the images in the backward's last kernel)
+    return (gnorm::workgroups(*s, g) + s->channels / 16 + 1) * gnorm::threads_of(g) < (int64_t)1 << 32 ? CBR_OK : CBR_E_UNSUPPORTED;
 }
 
 // Workspace bytes, rounded up.

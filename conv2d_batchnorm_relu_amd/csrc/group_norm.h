@@ -12,12 +12,10 @@ using namespace bnorm;   // Row, load_vec, the lane sums
 // One workgroup takes `ng` neighbouring groups (a chunk: w = ng * cpg channels, fewer in the last
 // one) of `ipw` images, or of one tile of one image's pixels.  Thread (sub, prow, vec) holds the
 // chunk's channels 8 vec .. + 7 of image sub, at pixels prow, prow + P, ...: k of them, all in registers
-// from the first load to the last store (a tile's in turns of the kernel's K).
-// Pixels a thread holds, of fp32 (twice of 16-bit types), in one of a tile's turns and of an image held whole: what fits
-// 128 registers with a thread's eight channels in one group, in two at most, or each for itself (nv 1, 2, 8).
-__host__ __device__ constexpr int fwd_turn(int nv) { return nv == 1 ? 3 : 2; }
+// from the first load to the last store (a tile's one after the other).
+// Pixels a thread holds of an image held whole, of fp32 (twice of 16-bit types): what fits 128 registers with a thread's
+// eight channels in one group, in two at most, or each for itself (nv 1, 2, 8).
 __host__ __device__ constexpr int fwd_most(int nv) { return nv == 1 ? 10 : nv == 2 ? 8 : 6; }
-__host__ __device__ constexpr int bwd_turn(int nv) { return nv == 1 ? 2 : 1; }
 __host__ __device__ constexpr int bwd_most(int nv) { return nv == 1 ? 4 : nv == 2 ? 3 : 2; }
 
 struct Geo {
@@ -79,6 +77,8 @@ struct Thread {
         on = image < p.images && 8 * vec < at.w;
         left = on ? rows - prow : 0;
     }
+    // how many of the k pixels are the thread's
+    __device__ __forceinline__ int pixels(const Geo &g) const { return left > 0 ? min(g.k, (left + g.P - 1) / g.P) : 0; }
 };
 
 // A workgroup's part of a tensor: whole chunks of eight channels through a buffer, whose offsets need one

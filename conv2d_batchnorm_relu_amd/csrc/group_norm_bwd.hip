@@ -189,31 +189,25 @@ __global__ __launch_bounds__(1024) void gn_bwd_kernel(GroupNormArgs p)
     });
 }
 
-// K of a thread's pixels of x and dy.
-template <typename T, Tail TAIL, int K>
+// A pixel of x and dy.
+template <typename T, Tail TAIL>
 struct Pair {
-    Raw8<T> x[K], d[K];
-    __device__ __forceinline__ void fetch(const Part<T, TAIL> &ix, const Part<T, TAIL> &id, const Geo &g, const Thread &me, int i0)
+    Raw8<T> x, d;
+    __device__ __forceinline__ void fetch(const Part<T, TAIL> &ix, const Part<T, TAIL> &id, int i, bool on)
     {
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const bool on = (i0 + i) * g.P < me.left && i0 + i < g.k;
-            ix.load(x[i], i0 + i, on);
-            id.load(d[i], i0 + i, on);
-        }
+        ix.load(x, i, on);
+        id.load(d, i, on);
     }
     __device__ __forceinline__ void settle(const Part<T, TAIL> &ix)
     {
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            ix.settle(x[i]);
-            ix.settle(d[i]);
-        }
+        ix.settle(x);
+        ix.settle(d);
     }
 };
 
-// First kernel of large images: a tile's S1 and S0 of each channel.
-template <typename T, Tail TAIL, int NV, int K>
+// First kernel of large images: a tile's S1 and S0 of each channel.  One pixel is on its way while another is added: more
+// of them cost waves (four and four, bf16: 64 x 56 x 56 x 256 111 us; two and two 99; one and one 96).
+template <typename T, Tail TAIL, int NV>
 __global__ __launch_bounds__(1024) void gn_bwd_tiles_kernel(GroupNormArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) float lds[];
@@ -222,22 +216,21 @@ __global__ __launch_bounds__(1024) void gn_bwd_tiles_kernel(GroupNormArgs p)
     const Thread me(p, at);
     const Part<T, TAIL> ix(p.x, me.first, me.prow, p.C, g.P, me.vec, at.w), id(p.dy, me.first, me.prow, p.C, g.P, me.vec, at.w);
     const Split<NV> sp(me.vec, p.cpg, at.ngl);
-    Pair<T, TAIL, K> one, two;
-    one.fetch(ix, id, g, me, 0);   // one turn is on its way while the other is added
+    const int own = me.pixels(g);
+    Pair<T, TAIL> one, two;
+    one.fetch(ix, id, 0, 0 < own);
     Coef<NV> cf;
     cf.template load<TAIL>(p, at, me, sp);
     float s1[8] = {}, s0[8] = {};
-    auto add = [&](Pair<T, TAIL, K> &r, int i0) __attribute__((always_inline)) {
+    auto add = [&](Pair<T, TAIL> &r, int i) __attribute__((always_inline)) {
         r.settle(ix);
-#pragma unroll
-        for (int i = 0; i < K; ++i)
-            if ((i0 + i) * g.P < me.left && i0 + i < g.k) add_pixel<T, NV>(cf, r.x[i], r.d[i], sp, p.act, s1, s0);
+        if (i < own) add_pixel<T, NV>(cf, r.x, r.d, sp, p.act, s1, s0);
     };
-    for (int i0 = 0; i0 < g.k; i0 += 2 * K) {
-        two.fetch(ix, id, g, me, i0 + K);
-        add(one, i0);
-        one.fetch(ix, id, g, me, i0 + 2 * K);
-        add(two, i0 + K);
+    for (int i = 0; i < g.k; i += 2) {
+        two.fetch(ix, id, i + 1, i + 1 < own);
+        add(one, i);
+        one.fetch(ix, id, i + 2, i + 2 < own);
+        add(two, i + 1);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) s1[e] *= sp.pick(cf.inv, e);
@@ -309,7 +302,7 @@ __global__ __launch_bounds__(1024) void gn_bwd_finish_kernel(GroupNormArgs p)
 inline __host__ __device__ int apply_parts(const Geo &g) { return max(1, min(g.V * g.P / (16 * g.V), 8)); }
 inline int apply_floats(const Geo &g) { return 16 * g.V * (apply_parts(g) + 1) + 2 * g.ng; }
 
-template <typename T, Tail TAIL, int NV, int K>
+template <typename T, Tail TAIL, int NV>
 __global__ __launch_bounds__(1024) void gn_bwd_apply_kernel(GroupNormArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) float lds[];
@@ -322,8 +315,9 @@ __global__ __launch_bounds__(1024) void gn_bwd_apply_kernel(GroupNormArgs p)
     const Thread me(p, at);
     const Part<T, TAIL> ix(p.x, me.first, me.prow, p.C, g.P, me.vec, at.w), id(p.dy, me.first, me.prow, p.C, g.P, me.vec, at.w),
         out(p.out, me.first, me.prow, p.C, g.P, me.vec, at.w);
-    Pair<T, TAIL, K> one, two;
-    one.fetch(ix, id, g, me, 0);
+    const int own = me.pixels(g);
+    Pair<T, TAIL> one, two;
+    one.fetch(ix, id, 0, 0 < own);
     const Split<NV> sp(me.vec, p.cpg, at.ngl);
     Coef<NV> cf;
     cf.template load<TAIL>(p, at, me, sp);
@@ -366,20 +360,17 @@ __global__ __launch_bounds__(1024) void gn_bwd_apply_kernel(GroupNormArgs p)
         c1[e] = tot[sp.gi[e]] * m * cf.inv[e] * cf.inv[e];
         c0[e] = tot[g.ng + sp.gi[e]] * m * cf.inv[e];
     }
-    auto finish = [&](Pair<T, TAIL, K> &r, int i0) __attribute__((always_inline)) {
+    auto finish = [&](Pair<T, TAIL> &r, int i) __attribute__((always_inline)) {
+        float x[8];
         r.settle(ix);
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            float x[8];
-            dx_of<T, NV>(cf, r.x[i], r.d[i], sp, p.act, c1, c0, x);
-            out.store(x, i0 + i, (i0 + i) * g.P < me.left && i0 + i < g.k, p.nt);
-        }
+        dx_of<T, NV>(cf, r.x, r.d, sp, p.act, c1, c0, x);
+        out.store(x, i, i < own, p.nt);
     };
-    for (int i0 = 0; i0 < g.k; i0 += 2 * K) {
-        two.fetch(ix, id, g, me, i0 + K);
-        finish(one, i0);
-        one.fetch(ix, id, g, me, i0 + 2 * K);
-        finish(two, i0 + K);
+    for (int i = 0; i < g.k; i += 2) {
+        two.fetch(ix, id, i + 1, i + 1 < own);
+        finish(one, i);
+        one.fetch(ix, id, i + 2, i + 2 < own);
+        finish(two, i + 1);
     }
 }
 
@@ -396,17 +387,17 @@ hipError_t launch_with(Kern k, const GroupNormArgs &a, int lds, hipStream_t st)
 template <typename T, Tail TAIL, int NV>
 hipError_t launch_tail(const GroupNormArgs &a, hipStream_t st)
 {
-    constexpr int B = 4 / T::SIZE, TURN = bwd_turn(NV) * B;
+    constexpr int B = 4 / T::SIZE;
     const Geo &g = a.g;
     const int lds = bwd_floats(g, a.cpg) * (int)sizeof(float), fin = a.part && (a.dw || a.db) ? (a.C + FC - 1) / FC : 0;
     hipError_t e;
     if (g.tiles > 1) {
-        e = launch_with(gn_bwd_tiles_kernel<T, TAIL, NV, TURN>, a, lds, st);
+        e = launch_with(gn_bwd_tiles_kernel<T, TAIL, NV>, a, lds, st);
         if (e != hipSuccess) return e;
         if (a.out) {
             GroupNormArgs b = a;
             b.front = fin;
-            return launch_with(gn_bwd_apply_kernel<T, TAIL, NV, TURN>, b, std::max(apply_floats(g) * (int)sizeof(float), fin ? threads_of(g) * 16 : 0), st);
+            return launch_with(gn_bwd_apply_kernel<T, TAIL, NV>, b, std::max(apply_floats(g) * (int)sizeof(float), fin ? threads_of(g) * 16 : 0), st);
         }
     } else if (g.k <= B) {
         e = launch_with(gn_bwd_kernel<T, TAIL, NV, B>, a, lds, st);

@@ -120,10 +120,10 @@ __global__ __launch_bounds__(1024) void gn_fwd_kernel(GroupNormArgs p)
         }
 }
 
-// First kernel of large images: each group's (mean, M2) of a tile.  A thread takes the means of the channels it
-// holds over its pixels of a turn, then the squares about them, and joins them to those of its earlier turns (every
-// channel for itself: eight chains of sums side by side).
-template <typename T, Tail TAIL, int NV, int K>
+// First kernel of large images: each group's (mean, M2) of a tile.  A thread runs the mean and the squares about it of every
+// channel over its pixels (Welford's recurrence: eight chains side by side).  One pixel is on its way while another is
+// added: more of them cost waves (four and four, bf16: 4 x 112 x 112 x 480 48 us; one and one 34).
+template <typename T, Tail TAIL, int NV>
 __global__ __launch_bounds__(1024) void gn_fwd_tiles_kernel(GroupNormArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) float lds[];
@@ -131,52 +131,29 @@ __global__ __launch_bounds__(1024) void gn_fwd_tiles_kernel(GroupNormArgs p)
     const Geo &g = p.g;
     const Thread me(p, at);
     const Part<T, TAIL> in(p.x, me.first, me.prow, p.C, g.P, me.vec, at.w);
+    const int own = me.pixels(g);
     float mean[8] = {}, m2[8] = {}, n = 0.f;
-    Raw8<T> one[K], two[K];
-    auto fetch = [&](Raw8<T>(&raw)[K], int i0) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < K; ++i) in.load(raw[i], i0 + i, (i0 + i) * g.P < me.left && i0 + i < g.k);
-    };
-    auto add = [&](Raw8<T>(&raw)[K], int i0) __attribute__((always_inline)) {
-        const int have = min(min(K, g.k - i0), max(0, (me.left + g.P - 1) / g.P - i0));   // of the K pixels
-        if (have <= 0) return;
-        const float now = (float)have, rn = 1.f / now, share = now / (n + now);
-        float s[8] = {}, q[8] = {};
-#pragma unroll
-        for (int i = 0; i < K; ++i) {   // (what is not there was loaded as zeros)
-            float v[8];
-            in.settle(raw[i]);
-            unpack8<T>(raw[i], v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] += v[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] *= rn;
-#pragma unroll
-        for (int i = 0; i < K; ++i)
-            if (i < have) {
-                float v[8];
-                unpack8<T>(raw[i], v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float d = v[e] - s[e];
-                    q[e] = fmaf(d, d, q[e]);
-                }
-            }
+    Raw8<T> one, two;
+    auto add = [&](Raw8<T> &raw, int i) __attribute__((always_inline)) {
+        if (i >= own) return;
+        float v[8];
+        in.settle(raw);
+        unpack8<T>(raw, v);
+        n += 1.f;
+        const float share = 1.f / n;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float d = s[e] - mean[e];
+            const float d = v[e] - mean[e];
             mean[e] = fmaf(d, share, mean[e]);
-            m2[e] += fmaf(d * d, n * share, q[e]);
+            m2[e] = fmaf(d, v[e] - mean[e], m2[e]);
         }
-        n += now;
     };
-    fetch(one, 0);   // one turn is on its way while the other is added
-    for (int i0 = 0; i0 < g.k; i0 += 2 * K) {
-        fetch(two, i0 + K);
-        add(one, i0);
-        fetch(one, i0 + 2 * K);
-        add(two, i0 + K);
+    in.load(one, 0, 0 < own);
+    for (int i = 0; i < g.k; i += 2) {
+        in.load(two, i + 1, i + 1 < own);
+        add(one, i);
+        in.load(one, i + 2, i + 2 < own);
+        add(two, i + 1);
     }
     // Over the channels and threads: the mean of the means, then the squares about it
     GroupSum<NV, 1> sum(p, lds, me);
@@ -200,7 +177,7 @@ __global__ __launch_bounds__(1024) void gn_fwd_tiles_kernel(GroupNormArgs p)
 }
 
 // Second kernel of large images: the tiles' statistics joined, then the tile's y.
-template <typename T, Tail TAIL, int NV, int K>
+template <typename T, Tail TAIL, int NV>
 __global__ __launch_bounds__(1024) void gn_fwd_apply_kernel(GroupNormArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) float lds[];   // [ng][2]
@@ -208,12 +185,9 @@ __global__ __launch_bounds__(1024) void gn_fwd_apply_kernel(GroupNormArgs p)
     const Geo &g = p.g;
     const Thread me(p, at);
     const Part<T, TAIL> in(p.x, me.first, me.prow, p.C, g.P, me.vec, at.w), out(p.out, me.first, me.prow, p.C, g.P, me.vec, at.w);
-    Raw8<T> one[K], two[K];
-    auto fetch = [&](Raw8<T>(&raw)[K], int i0) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < K; ++i) in.load(raw[i], i0 + i, (i0 + i) * g.P < me.left && i0 + i < g.k);
-    };
-    fetch(one, 0);
+    const int own = me.pixels(g);
+    Raw8<T> one, two;
+    in.load(one, 0, 0 < own);
     Coef<NV> cf;
     load_vec<8, TAIL>(p.w ? p.w + at.c0 : nullptr, 1.f, me.vec, g.V, at.w, cf.a);
     load_vec<8, TAIL>(p.b ? p.b + at.c0 : nullptr, 0.f, me.vec, g.V, at.w, cf.b);
@@ -252,21 +226,18 @@ __global__ __launch_bounds__(1024) void gn_fwd_apply_kernel(GroupNormArgs p)
         inv[e] = lds[2 * sp.gi[e] + 1];
     }
     cf.set(inv, sp, p.act);
-    auto finish = [&](Raw8<T>(&raw)[K], int i0) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            float v[8];
-            in.settle(raw[i]);
-            unpack8<T>(raw[i], v);
-            cf.apply(v, sp, p.act);
-            out.store(v, i0 + i, (i0 + i) * g.P < me.left && i0 + i < g.k, p.nt);
-        }
+    auto finish = [&](Raw8<T> &raw, int i) __attribute__((always_inline)) {
+        float v[8];
+        in.settle(raw);
+        unpack8<T>(raw, v);
+        cf.apply(v, sp, p.act);
+        out.store(v, i, i < own, p.nt);
     };
-    for (int i0 = 0; i0 < g.k; i0 += 2 * K) {
-        fetch(two, i0 + K);
-        finish(one, i0);
-        fetch(one, i0 + 2 * K);
-        finish(two, i0 + K);
+    for (int i = 0; i < g.k; i += 2) {
+        in.load(two, i + 1, i + 1 < own);
+        finish(one, i);
+        in.load(one, i + 2, i + 2 < own);
+        finish(two, i + 1);
     }
 }
 
@@ -283,12 +254,12 @@ hipError_t launch_with(Kern k, const GroupNormArgs &a, int lds, hipStream_t st)
 template <typename T, Tail TAIL, int NV>
 hipError_t launch_tail(const GroupNormArgs &a, hipStream_t st)
 {
-    constexpr int B = 4 / T::SIZE, TURN = fwd_turn(NV) * B;   // a vector takes 4 registers of 16-bit types, 8 of fp32
+    constexpr int B = 4 / T::SIZE;   // a vector takes 4 registers of 16-bit types, 8 of fp32
     const int lds = sum_floats(a.g, NV, 1) * (int)sizeof(float), k = a.g.k;
     if (a.g.tiles > 1) {
-        const hipError_t e = launch_with(gn_fwd_tiles_kernel<T, TAIL, NV, TURN>, a, lds, st);
+        const hipError_t e = launch_with(gn_fwd_tiles_kernel<T, TAIL, NV>, a, lds, st);
         if (e != hipSuccess) return e;
-        return launch_with(gn_fwd_apply_kernel<T, TAIL, NV, TURN>, a, 2 * a.g.ng * (int)sizeof(float), st);
+        return launch_with(gn_fwd_apply_kernel<T, TAIL, NV>, a, 2 * a.g.ng * (int)sizeof(float), st);
     }
     if (k <= 2 * B) return launch_with(gn_fwd_kernel<T, TAIL, NV, 2 * B>, a, lds, st);
     if (k <= 4 * B) return launch_with(gn_fwd_kernel<T, TAIL, NV, 4 * B>, a, lds, st);

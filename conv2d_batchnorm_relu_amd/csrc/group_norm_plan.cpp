@@ -18,7 +18,7 @@ double expected_us(const cbr_group_norm_shape &s, const Geo &g, bool backward, i
     auto up = [](double a, double b) { return (double)(int64_t)((a + b - 1) / b); };
     const int f = 4 / size, t = threads_of(g);
     const bool tiled = g.tiles > 1;
-    const int waves = tiled ? 16 : backward ? (g.k <= f ? 24 : g.k <= 2 * f ? 20 : 16) : g.k <= 2 * f ? 32 : g.k <= 4 * f ? 24 : 16;
+    const int waves = tiled ? (backward ? 20 : 32) : backward ? (g.k <= f ? 24 : g.k <= 2 * f ? 20 : 16) : g.k <= 2 * f ? 32 : g.k <= 4 * f ? 24 : 16;
     const double share = std::max(1, waves * 64 / std::max(t, 64)), wgs = (double)workgroups(s, g);
     const double act = std::min(share, up(wgs, 256.)), waves_of = up(t, 64.);
     const double values = (double)g.ipw * std::min<int64_t>(s.pixels, (int64_t)g.P * g.k) * g.ng * cpg;
@@ -27,8 +27,8 @@ double expected_us(const cbr_group_norm_shape &s, const Geo &g, bool backward, i
     const bool large = (double)s.images * s.pixels * s.channels * size > 32e6;   // past the L2s: runs of a part of a line cost more
     const double narrow = width >= 128 ? 1. : width >= 64 ? (large ? 1.05 : 1.02) : width >= 32 ? (large ? 1.35 : 1.14) : large ? 1.7 : 1.26;
     const double passes = tiled ? (backward ? 5. : 3.) : backward ? 3. : 2.;
-    const double turn = (backward ? 2 * bwd_turn(nv) : fwd_turn(nv)) * f, held = g.k * (backward ? 2. : 1.);
-    const double flying = t * act * std::min(held, tiled ? 1.5 * turn : held) * 8 * size / 1.32;
+    const double each = backward ? 2. : 1.;
+    const double flying = t * act * (tiled ? std::min<double>(g.k, 1.5) : g.k) * each * 8 * size / 1.32;
     const double rate = std::min(std::min(71e3, flying), 5.0e6 / std::min(wgs, 256.));
     const double mem = act * values * size * passes * narrow / rate;
     // arithmetic: instructions a value and pass

@@ -9,10 +9,10 @@ namespace cbr {
 namespace gnorm {
 namespace {
 
-// Expected time of a layout in us, fitted to some 5000 measurements (60 shapes, up to 55 layouts each; the layout it
-// picks takes 5% longer than the fastest one in the mean, 1.3 times as long at worst).  Workgroups run in rounds of as
-// many as the registers let share the CUs; in a round a CU's loads and stores and its arithmetic overlap only in part, and
-// a workgroup alone on its CU loads, sums and stores one after the other.
+// Expected time of a layout in us, fitted to some 13000 measurements (180 shapes of both passes, up to 55 layouts each;
+// the layout it picks takes 4% longer than the fastest one in the mean, 5% on shapes that were left out of the fit, 1.6
+// times as long at worst).  Workgroups run in rounds of as many as the registers let share the CUs; in a round a CU's loads
+// and stores and its arithmetic overlap only in part, and a workgroup alone on its CU loads, sums and stores one after the other.
 double expected_us(const cbr_group_norm_shape &s, const Geo &g, bool backward, int cpg, int nv, int size)
 {
     auto up = [](double a, double b) { return (double)(int64_t)((a + b - 1) / b); };
@@ -22,26 +22,25 @@ double expected_us(const cbr_group_norm_shape &s, const Geo &g, bool backward, i
     const double share = std::max(1, waves * 64 / std::max(t, 64)), wgs = (double)workgroups(s, g);
     const double act = std::min(share, up(wgs, 256.)), waves_of = up(t, 64.);
     const double values = (double)g.ipw * std::min<int64_t>(s.pixels, (int64_t)g.P * g.k) * g.ng * cpg;
-    // memory: bytes over what a CU gets, 71 GB/s or its share of 5 TB/s, and what its loads in flight carry
+    // memory: bytes over what a CU gets, 30 or 37 GB/s or its share of 5 TB/s, and what its loads in flight carry
     const double width = (double)g.ng * cpg * size;
-    const bool large = (double)s.images * s.pixels * s.channels * size > 32e6;   // past the L2s: runs of a part of a line cost more
-    const double narrow = width >= 128 ? 1. : width >= 64 ? (large ? 1.05 : 1.02) : width >= 32 ? (large ? 1.35 : 1.14) : large ? 1.7 : 1.26;
+    const double narrow = width >= 128 ? 1. : width >= 64 ? 1.02 : width >= 32 ? 1.28 : 1.55;   // runs of a part of a line
     const double passes = tiled ? (backward ? 5. : 3.) : backward ? 3. : 2.;
-    const double each = backward ? 2. : 1.;
-    const double flying = t * act * (tiled ? std::min<double>(g.k, 1.5) : g.k) * each * 8 * size / 1.32;
-    const double rate = std::min(std::min(71e3, flying), 5.0e6 / std::min(wgs, 256.));
+    const double flying = t * act * (tiled ? std::min<double>(g.k, 1.5) / 0.6 : g.k / 0.165) * (backward ? 2. : 1.) * 8 * size;
+    const double rate = std::min(std::min(tiled ? 29.5e3 : 37e3, flying), 5.0e6 / std::min(wgs, 256.));
     const double mem = act * values * size * passes * narrow / rate;
     // arithmetic: instructions a value and pass
-    const double ins = (s.act == CBR_ACT_SILU ? (backward ? 37. : 19.7) : backward ? 13. : 9.) * (nv > 1 ? 5.5 : 1.);
-    const double alu = std::max(1., waves_of * act / 4.) * g.k * ins * 0.0057;
+    const double ins = (s.act == CBR_ACT_SILU ? (backward ? 41. : 21.4) : backward ? 13. : 9.) * (nv > 1 ? 5. : 1.);
+    const double alu = std::max(1., waves_of * act / 4.) * g.k * ins * (tiled ? 0.00073 : 0.0026);
     // the sums over a workgroup, and what the second kernel of large images reads before it begins
-    const double sums = 0.19 * (tiled ? 2 : 1) * (g.pre ? 1 : 2) * up(t, 256.);
-    const double join = !tiled ? 0. : 0.38 * up(g.tiles, 64.) * (backward ? up(g.V * 128., t) : up(g.ng, std::max(t / 64, 1)));
-    const double rounds = std::max(1., wgs / (256. * share)), whole = rounds < 6. ? 0.18 * up(wgs, 256. * share) + 0.82 * rounds : rounds;
-    double one = 1.5 + sums + join + std::max(mem, alu) + (tiled ? 0.1 : 2.4) * std::min(mem, alu);
-    if (!tiled && act == 1. && rounds > 1.) one += 0.16 * mem;
-    if (tiled && large && t < 512) one *= 1.08;   // (fewer waves to a CU)
-    return 2.3 + (tiled ? 4.6 : 0.) + (backward && s.images * g.tiles > 1 ? (tiled ? 0.8 : 3.1) : 0.) + whole * one;
+    const double sums = 0.113 * (tiled ? 2 : 1) * (g.pre ? 1 : 2) * up(t, 256.);
+    const double join = !tiled ? 0. : 0.28 * up(g.tiles, 64.) * (backward ? up(g.V * 128., t) : up(g.ng, std::max(t / 64, 1)));
+    const double rounds = std::max(1., wgs / (256. * share)), whole = rounds < 6. ? 0.08 * up(wgs, 256. * share) + 0.92 * rounds : rounds;
+    double one = 0.52 + sums + join + std::max(mem, alu) + (tiled ? 0.09 : 2.25) * std::min(mem, alu);
+    if (!tiled && act == 1. && rounds > 1.) one += 0.09 * mem;
+    // (large maps by fewer than eight waves a CU: 4 x 112 x 112 x 512 backward 70 us, with eight 52)
+    if (tiled && t * act < 512 && (double)s.images * s.pixels * s.channels * size > 32e6) one *= 1.1;
+    return 4.7 + (tiled ? 1.4 : 0.) + (backward && s.images * g.tiles > 1 ? (tiled ? 0.8 : 3.9) : 0.) + whole * one;
 }
 
 Geo least_time(const cbr_group_norm_shape &s, bool backward)

@@ -116,7 +116,8 @@ __device__ __forceinline__ void settle8(int64_t col, int64_t cols, Raw8<T> &r)
 }
 
 // Groups of a row: four lanes a group, eight values each; sixteen lanes the four groups of 128 values
-// whose scales make a word.  A workgroup takes one column of those over 16 U rows.
+// whose scales make a word.  A workgroup takes one column of those over 16 U rows.  (64 x 2048 bf16: 2.7 us, a launch and
+// a load.)
 template <typename T, bool TAIL, int U>
 __global__ __launch_bounds__(NT) void quant4_rows_kernel(const char *__restrict__ src, int64_t rows, int64_t cols, int64_t ldq,
                                                          int kbs, uint8_t *__restrict__ q, uint32_t *__restrict__ scale)
@@ -152,7 +153,8 @@ __global__ __launch_bounds__(NT) void quant4_rows_kernel(const char *__restrict_
 
 // The transpose: a tile of 256 x 64 source values.  Thread (cl, rl) of 8 x 32 holds rows 8 rl .. + 7 of columns
 // 8 cl .. + 7; four lanes, eight apart, hold a group of each of their columns.  The codes are turned over in
-// LDS: 128 bytes of a column, padded to 132.
+// LDS: 128 bytes of a column, padded to 132.  Bound by memory: 50176 x 1024 bf16 21 us, 6.1 TB/s (a part of it from the
+// caches).
 constexpr int TR = 256, TC = 64, LROW = TR / 8 + 1;
 
 template <typename T, bool TAIL>
@@ -217,48 +219,37 @@ __global__ __launch_bounds__(NT) void quant4_turned_kernel(const char *__restric
     }
 }
 
-// Back: eight values a thread.
-template <typename T, bool TAIL, int U>
+// Back: eight values a thread.  Bound by memory (50176 x 1024 to bf16: 24 us, 5.4 TB/s; four rows a thread were no faster,
+// 4096 x 512 3.8 us instead of 3.2).
+template <typename T, bool TAIL>
 __global__ __launch_bounds__(NT) void dequant4_kernel(const uint8_t *__restrict__ q, const uint32_t *__restrict__ scale, int64_t rows,
                                                       int64_t cols, int64_t ldq, int kbs, char *__restrict__ v)
 {
-    const int64_t kb = blockIdx.x % kbs, row0 = (int64_t)(blockIdx.x / kbs) * (16 * U);
-    const int lane = threadIdx.x % 16, sub = threadIdx.x / 16;
-    const int64_t col = kb * 128 + lane * 8;
-    uint32_t code[U], word[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t row = row0 + u * 16 + sub;
-        const bool on = row < rows && col < cols;
-        code[u] = on ? *(const uint32_t *)(q + row * ldq + col / 2) : 0u;
-        word[u] = on ? scale[kb * rows + row] : 0u;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t row = row0 + u * 16 + sub;
-        if (row >= rows || col >= cols) continue;
-        const uint32_t byte = word[u] >> (8 * (lane / 4)) & 255u;
-        const float s = scale_of(byte);
-        float o[8];
-        auto two = [&](auto sc) __attribute__((always_inline)) {
-            constexpr int S = decltype(sc)::value;
-            // unscaled and then multiplied: exact, also for numbers below fp32's normal ones
-            const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[u], 1.f, S);
-            o[2 * S] = byte == 255 ? __builtin_nanf("") : p[0] * s;
-            o[2 * S + 1] = byte == 255 ? __builtin_nanf("") : p[1] * s;
-        };
-        two(std::integral_constant<int, 0>{});
-        two(std::integral_constant<int, 1>{});
-        two(std::integral_constant<int, 2>{});
-        two(std::integral_constant<int, 3>{});
-        char *p = v + (row * cols + col) * T::SIZE;
-        if (!TAIL || col + 8 <= cols) {
-            Raw8<T> r;
-            pack8<T>(o, r);
-            store_raw8<T, TAIL>(p, r);
-        } else {
-            store_part8<T>(p, (int)(cols - col), o);
-        }
+    const int64_t kb = blockIdx.x % kbs;
+    const int lane = threadIdx.x % 16;
+    const int64_t row = (int64_t)(blockIdx.x / kbs) * 16 + threadIdx.x / 16, col = kb * 128 + lane * 8;
+    if (row >= rows || col >= cols) return;
+    const uint32_t code = *(const uint32_t *)(q + row * ldq + col / 2), byte = scale[kb * rows + row] >> (8 * (lane / 4)) & 255u;
+    const float s = scale_of(byte);
+    float o[8];
+    auto two = [&](auto sc) __attribute__((always_inline)) {
+        constexpr int S = decltype(sc)::value;
+        // unscaled and then multiplied: exact, also for numbers below fp32's normal ones
+        const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.f, S);
+        o[2 * S] = byte == 255 ? __builtin_nanf("") : p[0] * s;
+        o[2 * S + 1] = byte == 255 ? __builtin_nanf("") : p[1] * s;
+    };
+    two(std::integral_constant<int, 0>{});
+    two(std::integral_constant<int, 1>{});
+    two(std::integral_constant<int, 2>{});
+    two(std::integral_constant<int, 3>{});
+    char *p = v + (row * cols + col) * T::SIZE;
+    if (!TAIL || col + 8 <= cols) {
+        Raw8<T> r;
+        pack8<T>(o, r);
+        store_raw8<T, TAIL>(p, r);
+    } else {
+        store_part8<T>(p, (int)(cols - col), o);
     }
 }
 
@@ -271,8 +262,9 @@ hipError_t launch_quant(const cbr_fp4_shape &s, const char *src, uint8_t *q, uin
                       s.rows, s.cols, s.ldq, (int)ctiles, q, scale);
     }
     const int64_t kbs = (s.cols + 127) / 128;
-    // Four rows a thread once that still leaves a workgroup for every CU
-    const bool four = (s.rows + 63) / 64 * kbs >= 256;
+    // Four rows a thread where that leaves a CU four workgroups (20000 x 2048 20.0 us, one row 21.3; 4096 x 512, a
+    // workgroup a CU, 3.6 and 3.2)
+    const bool four = (s.rows + 63) / 64 * kbs >= 1024;
     const int64_t tiles = (s.rows + (four ? 63 : 15)) / (four ? 64 : 16);
     return launch(four ? quant4_rows_kernel<T, TAIL, 4> : quant4_rows_kernel<T, TAIL, 1>, dim3((uint32_t)(tiles * kbs)), dim3(NT), 0,
                   st, nullptr, nullptr, src, s.rows, s.cols, s.ldq, (int)kbs, q, (uint32_t *)scale);
@@ -282,10 +274,8 @@ template <typename T, bool TAIL>
 hipError_t launch_back(const cbr_fp4_shape &s, const uint8_t *q, const uint8_t *scale, char *v, hipStream_t st)
 {
     const int64_t rows = s.transpose ? s.cols : s.rows, cols = s.transpose ? s.rows : s.cols, kbs = (cols + 127) / 128;
-    const bool four = (rows + 63) / 64 * kbs >= 256;
-    const int64_t tiles = (rows + (four ? 63 : 15)) / (four ? 64 : 16);
-    return launch(four ? dequant4_kernel<T, TAIL, 4> : dequant4_kernel<T, TAIL, 1>, dim3((uint32_t)(tiles * kbs)), dim3(NT), 0, st,
-                  nullptr, nullptr, q, (const uint32_t *)scale, rows, cols, s.ldq, (int)kbs, v);
+    return launch(dequant4_kernel<T, TAIL>, dim3((uint32_t)((rows + 15) / 16 * kbs)), dim3(NT), 0, st, nullptr, nullptr, q,
+                  (const uint32_t *)scale, rows, cols, s.ldq, (int)kbs, v);
 }
 
 }  // namespace

@@ -344,8 +344,8 @@ inline int64_t workgroups(const cbr_group_norm_shape &s, const Geo &g)
 }
 inline int threads_of(const Geo &g) { return g.V * g.P * g.ipw; }
 // Outputs past the caches' 32 MB are written as streams (the next call would not find them there): 256 x 28 x 28 x 512
-// forward 89 -> 84 us, 8 x 224 x 224 x 64 fp32 backward 113 -> 101.  Not in runs of fewer than 64 bytes, which the caches
-// have to put together (64 x 56 x 56 x 256 backward in runs of 32: 129 -> 150 us).
+// forward 92 -> 90 us, 8 x 224 x 224 x 64 fp32 backward 113 -> 98, 64 x 56 x 56 x 256 backward 109 -> 95.  Not in runs of fewer than 64 bytes, which the caches
+// have to put together (64 x 56 x 56 x 256 backward held whole, in runs of 32: 129 -> 150 us).
 inline bool streams(const cbr_group_norm_shape &s, const Geo &g)
 {
     const int size = s.type == CBR_F32 ? 4 : 2;

@@ -52,7 +52,8 @@ __device__ __forceinline__ void leave_groups(const GroupNormArgs &p, const Place
         }
 }
 
-// Images held whole.
+// Images held whole.  Bound by memory (256 x 28 x 28 x 512 bf16: 84 us, 4.9 TB/s; a large copy reaches 5.0), small calls by
+// a chain of latencies: the load, two sums over the workgroup, the store (49 x 512: 5.5 us).
 template <typename T, Tail TAIL, int NV, int K>
 __global__ __launch_bounds__(1024) void gn_fwd_kernel(GroupNormArgs p)
 {
@@ -176,7 +177,9 @@ __global__ __launch_bounds__(1024) void gn_fwd_tiles_kernel(GroupNormArgs p)
     leave_groups<NV>(p, at, me, sp, p.part + ((me.image * p.G + at.chunk * g.ng) * g.tiles + at.tile) * 2, 2 * g.tiles, all, s[0]);
 }
 
-// Second kernel of large images: the tiles' statistics joined, then the tile's y.
+// Second kernel of large images: the tiles' statistics joined, then the tile's y.  (16 x 225 x 1001 f32 in 7 groups: 9.0 us
+// for the first kernel and 9.2 for this one, of which reading and writing takes 2.9 and 5.7: rows of 143 channels leave four
+// small workgroups a CU, all in the same phase.)
 template <typename T, Tail TAIL, int NV>
 __global__ __launch_bounds__(1024) void gn_fwd_apply_kernel(GroupNormArgs p)
 {

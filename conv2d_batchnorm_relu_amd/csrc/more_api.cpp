@@ -56,9 +56,9 @@ int check_fp4(const cbr_fp4_shape *s)
     if (s->rows > MAX_ROWS || s->cols > MAX_ROWS) return CBR_E_UNSUPPORTED;
     const int64_t v_cols = s->transpose ? s->rows : s->cols;
     if (s->ldq < (v_cols + 31) / 32 * 16 || s->ldq % 16) return CBR_E_SHAPE;
-    // one workgroup for each 64 rows and 128 columns (16 rows only where there are few)
-    if (((s->rows + 63) / 64) * ((s->cols + 127) / 128) >= MAX_GROUPS || ((s->rows + 127) / 128) * ((s->cols + 63) / 64) >= MAX_GROUPS)
-        return CBR_E_UNSUPPORTED;
+    // a workgroup for each 16 rows and 128 columns of v, or more of them
+    const int64_t v_rows = s->transpose ? s->cols : s->rows;
+    if (((v_rows + 15) / 16) * ((v_cols + 127) / 128) >= MAX_GROUPS) return CBR_E_UNSUPPORTED;
     return CBR_OK;
 }
 

@@ -426,8 +426,8 @@ int cbr_group_norm_backward(const cbr_group_norm_shape *shape, const void *dy, c
  * bytes past the last group are left as they are.  scale: one byte a group, the exponent plus
  * 127, [ceil(v_cols / 128)][v_rows][4]: the four groups of 128 values together; 127 (1) where
  * there is no group.  A NaN or infinity makes its group's scale 255 (NaN) and its values 0: the
- * group stands for NaN.  rows and cols positive, < 2^31, ceil(rows / 64) * ceil(cols / 128) and
- * ceil(rows / 128) * ceil(cols / 64) < 2^24 (CBR_E_UNSUPPORTED beyond that).  q and scale may
+ * group stands for NaN.  rows and cols positive, < 2^31, and
+ * ceil(v_rows / 16) * ceil(v_cols / 128) < 2^24 (CBR_E_UNSUPPORTED beyond that).  q and scale may
  * not overlap src or each other.
  */
 typedef struct cbr_fp4_shape {

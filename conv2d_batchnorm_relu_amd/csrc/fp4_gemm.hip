@@ -52,10 +52,16 @@ __device__ __forceinline__ uint32_t lds_word(uint32_t addr)
     return v;
 }
 
+// Position of a row's 16-byte chunks in LDS.  A read of 16 bytes a lane goes by sixteen lanes: of each 32 lanes those of
+// rows 0 to 3 and 12 to 15 with the next lane group's of rows 4 to 11, and the others.  Lane group g reads chunk 2 g
+// or 2 g + 1, so rows 4 to 11 have the upper half of the positions.  (With perm() itself, which suits chunk g, each read took
+// eight cycles instead of four.)
+__device__ constexpr int apart(int p) { return ((p >> 2 ^ p >> 1) & 1) << 2 | (p >> 2) << 1 | (p & 1); }
+
 // Tile kernel: 16 MS WM x 16 NS WN results a workgroup, WM x WN waves of 16 MS x 16 NS.  Both operands'
 // rows of a stage and their exponents come straight into LDS, NST stages deep, as in the 8-bit product.
 // 8192^3: 270 to 290 us, 4.1 to 3.8 PFLOP/s, with the clock down to 2 GHz by the power it takes; of it the loads alone take
-// 230 us (exponents, four bytes a lane: 17), the matrix instructions 182, the reads from LDS 155.  Smaller ones are
+// 230 us (exponents, four bytes a lane: 17), the matrix instructions 182, the reads from LDS 90.  Smaller ones are
 // bound by the way in and out of a workgroup: 50001 x 256 x 1024 17 us, of which 13 to 15 without any one of these.
 template <int BM, int BN>
 constexpr int word_row() { return (BM + BN) * 4 + 128; }   // words of a stage's half, 32 banks apart
@@ -91,7 +97,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm4_tile_kernel(Fp4Args p)
     const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void *)(p.b + (int64_t)n0 * p.ldb), 0,
                                                                         (int)((uint32_t)rows_b * p.ldb), 0x00020000);
     const int lrow = 8 * wave + (lane >> 3);
-    const int lchunk = 16 * ((lane & 7) ^ perm(lrow)), lchunk_b = 16 * ((lane & 7) ^ perm_b<F32>(lrow));
+    const int lchunk = 16 * ((lane & 7) ^ apart(perm(lrow))), lchunk_b = 16 * ((lane & 7) ^ apart(perm_b<F32>(lrow)));
     // (scalars of the wave: taken by value below, where a choice between captured ones would go through memory)
     const bool of_a = wave < NW / 2;
     const int first = of_a ? wave : wave - NW / 2, s_lds = of_a ? 0 : BM * 4;
@@ -124,9 +130,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm4_tile_kernel(Fp4Args p)
 #pragma unroll
         for (int j = 0; j < MS; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const uint32_t fa0 = lbase + (wm * 16 * MS + r16) * BK + 16 * (2 * g ^ perm(r16));
+    const uint32_t fa0 = lbase + (wm * 16 * MS + r16) * BK + 16 * (2 * g ^ apart(perm(r16)));
     const int brow = col_in_wave<F32>(0, r16 >> 2, r16 & 3);
-    const uint32_t fb0 = lbase + (BM + wn * 16 * NS + brow) * BK + 16 * (2 * g ^ perm_b<F32>(brow));
+    const uint32_t fb0 = lbase + (BM + wn * 16 * NS + brow) * BK + 16 * (2 * g ^ apart(perm_b<F32>(brow)));
     // exponents: the word with the lane's two groups, moved to its low bytes
     const uint32_t sa0 = lbase + WORDS + (g >> 1) * HALF + (wm * 16 * MS + r16) * 4;
     const uint32_t sb0 = lbase + WORDS + (g >> 1) * HALF + (BM + wn * 16 * NS + brow) * 4;

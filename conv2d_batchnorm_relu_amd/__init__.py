@@ -397,6 +397,8 @@ class _Call:
         """Address and bytes of a workspace (None: none; a pair is taken as they are)."""
         if workspace is None or isinstance(workspace, tuple):
             return _ws(workspace, self.where)
+        if workspace.get_device() == self.dev and workspace.is_contiguous():
+            return workspace.data_ptr(), workspace.nbytes
         if workspace.is_cuda and workspace.get_device() != self.torch.cuda.current_device():
             raise CbrError(_E_VALUE, self.where, "workspace is not on the current GPU")
         return _ws(workspace, self.where)

@@ -10,7 +10,7 @@ namespace gnorm {
 namespace {
 
 // Expected time of a layout in us, fitted to some 13000 measurements (180 shapes of both passes, up to 55 layouts each;
-// the layout it picks takes 4% longer than the fastest one in the mean, 5% on shapes that were left out of the fit, 1.6
+// the layout it picks takes 4% longer than the fastest one in the mean, 6% on shapes that were left out of the fit, 2.4
 // times as long at worst).  Workgroups run in rounds of as many as the registers let share the CUs; in a round a CU's loads
 // and stores and its arithmetic overlap only in part, and a workgroup alone on its CU loads, sums and stores one after the other.
 double expected_us(const cbr_group_norm_shape &s, const Geo &g, bool backward, int cpg, int nv, int size)

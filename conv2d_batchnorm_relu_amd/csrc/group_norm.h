@@ -84,7 +84,8 @@ struct Thread {
 // A workgroup's part of a tensor: whole chunks of eight channels through a buffer, whose offsets need one
 // register for all of a thread's pixels, and without branches: past the end loads read 0 and stores do
 // nothing.  (With 64-bit addresses and branches the forward took 40 registers more and held fewer pixels.)
-// Every part is shorter than 2^31 bytes.
+// Every offset formed is below 2^31, those of pixels that are switched off among them (least_time bounds them): what the
+// range check makes of a scalar offset past the buffer's end does not matter.
 template <typename T, Tail TAIL>
 struct Part {
     static constexpr int OOB = (int)0x80000000u;

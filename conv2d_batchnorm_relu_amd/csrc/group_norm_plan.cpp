@@ -81,18 +81,21 @@ Geo least_time(const cbr_group_norm_shape &s, bool backward)
                     best = g;
                 }
             };
-            const int64_t k = up(s.pixels, g.P);
-            g.ipw = (int)std::max<int64_t>(1, std::min<int64_t>({threads / (V * g.P), s.images, limit / s.pixels}));
-            if (k <= most && g.ipw * s.pixels <= limit) {
+            // Offsets of pixels past a part's end are formed too (their loads are switched off): of images held whole up to the
+            // last turn's end, of tiles two turns more (see the kernels' loops).
+            const int64_t k = up(s.pixels, g.P), held = k * g.P;
+            g.ipw = (int)std::max<int64_t>(1, std::min<int64_t>({threads / (V * g.P), s.images, (limit - held) / s.pixels + 1}));
+            if (k <= most && (g.ipw - 1) * s.pixels + held <= limit) {
                 g.tiles = 1;
                 g.k = (int)k;
                 weigh();
             }
             // tiles for one, two or four workgroups a CU (a small call is not worth a second kernel, nor weighing it)
             g.ipw = 1;
-            if (V * g.P < 64 || threads < 256 || k < 2 || (least > 0 && (double)s.images * s.pixels * s.channels < 250e3)) continue;
+            const int64_t turns = limit / g.P - 2;   // of a tile, at most
+            if (turns < 1 || V * g.P < 64 || threads < 256 || k < 2 || (least > 0 && (double)s.images * s.pixels * s.channels < 250e3)) continue;
             for (int64_t total = 256; total <= 1024; total *= 2) {
-                const int64_t tiles = std::max<int64_t>({2, up(s.pixels, g.P * std::max<int64_t>(1, limit / g.P)), std::min<int64_t>(k, total / (s.images * chunks))});
+                const int64_t tiles = std::max<int64_t>({2, up(s.pixels, g.P * turns), std::min<int64_t>(k, total / (s.images * chunks))});
                 g.k = (int)up(s.pixels, tiles * g.P);
                 g.tiles = (int)up(s.pixels, (int64_t)g.P * g.k);
                 if (g.tiles > 1) weigh();

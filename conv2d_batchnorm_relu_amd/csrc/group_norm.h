@@ -324,7 +324,12 @@ struct GroupSum {
 // sigmoid(u) = 1 / (1 + 2^v) comes as -ln 2 sigmoid(u) from a reciprocal of -log2(e) (1 + 2^v): the constants cost
 // nothing.  Both hardware functions are within one last place.
 constexpr float LOG2E = 1.44269504f, LN2 = 0.693147181f;
-__device__ __forceinline__ float scaled_sigmoid(float v) { return __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_exp2f(v), -LOG2E, -LOG2E)); }
+// power: 2^v
+__device__ __forceinline__ float scaled_sigmoid(float v, float &power)
+{
+    power = __builtin_amdgcn_exp2f(v);
+    return __builtin_amdgcn_rcpf(fmaf(power, -LOG2E, -LOG2E));
+}
 
 // LDS of the backward (floats): the groups' sums, and [rows][2][8 V ipw] sums of the channels.
 inline int bwd_floats(const Geo &g, int cpg) { return sum_floats(g, split_of(cpg), 2) + 2 * sum_rows(g) * 8 * g.V * g.ipw; }

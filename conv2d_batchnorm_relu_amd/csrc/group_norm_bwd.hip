@@ -31,9 +31,12 @@ struct Coef {
             if (act == CBR_ACT_RELU) {
                 g = u > 0.f ? dy : u <= 0.f ? 0.f : u;   // a NaN stays one
             } else {
-                const float s = scaled_sigmoid(u);   // -ln 2 sigmoid
-                // 1 + u (1 - sigmoid), with u = -ln 2 v
-                const float h = fmaf(u, -LN2 - s, 1.f);
+                float power;
+                const float s = scaled_sigmoid(u, power);   // -ln 2 sigmoid
+                // 1 + u (1 - sigmoid), with u = -ln 2 v: 1 - sigmoid as 2^v sigmoid, which keeps its digits where it is
+                // small (the difference from 1 lost them: the slope at 14 was off by 13 half steps).  Past the largest
+                // number s is 0.
+                const float h = fmaf(u, fminf(power, __FLT_MAX__) * s, 1.f);
                 g = dy * (SCALED ? s * h : (-LOG2E * s) * h);
             }
         }

@@ -34,7 +34,10 @@ struct Coef {
             for (int e = 0; e < 8; ++e) v[e] = v[e] < 0.f ? 0.f : v[e];   // a NaN stays one
         } else if (act == CBR_ACT_SILU) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= scaled_sigmoid(v[e]);
+            for (int e = 0; e < 8; ++e) {
+            float power;
+            v[e] *= scaled_sigmoid(v[e], power);
+        }
         }
     }
 };

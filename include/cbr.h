@@ -369,6 +369,7 @@ int cbr_gemm_fp8(const cbr_gemm_shape *shape, const void *a, const float *a_scal
  *   mean = mean of x, var = mean of (x - mean)^2 over pixels and channels (biased),
  *   xhat = (x - mean) / sqrt(var + eps),  u = xhat * w_c + b_c,  y = act(u)
  *   CBR_ACT_NONE: u;  CBR_ACT_RELU: max(u, 0), a NaN stays one;  CBR_ACT_SILU: u / (1 + e^-u).
+ * SiLU: |u| up to 2^127; values of y and of the slope below 2^-119 may become 0.
  * x, y, dx, dy have `type` (CBR_BF16, CBR_F16 or CBR_F32); w, b, their gradients and the
  * statistics are float.  Everything is computed in fp32 and rounded once.
  *

@@ -103,3 +103,14 @@ def test_drawn_sizes_keep_their_offsets(layout, near):
     r = random.Random(near)
     for _ in range(20000):
         check(layout, *drawn(r, near), r.choice((cbr.CBR_BF16, cbr.CBR_F16, cbr.CBR_F32)), r.random() < 0.5)
+
+
+def test_tiles_of_several_pixels_a_thread(layout):
+    """The sizes of tests/test_group_norm_tiles.py are laid out as it says."""
+    import test_group_norm_tiles as T
+    for size in T.TILES:
+        for dtype in (cbr.CBR_BF16, cbr.CBR_F32):
+            for backward in (False, True):
+                for act in (cbr.CBR_ACT_NONE, cbr.CBR_ACT_RELU, cbr.CBR_ACT_SILU):
+                    g = layout(*size, dtype, backward, act)
+                    assert g["tiles"] > 1 and 3 <= g["k"] <= T.MOST, (size, dtype, backward, act, g)

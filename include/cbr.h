@@ -452,8 +452,8 @@ int cbr_fp4_dequantize(const cbr_fp4_shape *shape, const void *q, const void *sc
  * values behind k in the last group are part of the sum and have to be zeros (in one of the operands at
  * least), what lies past the groups is not used.  lda, ldb multiples of 16, at least 16 * ceil(k / 32).
  * d [m][n] dense, d_type CBR_BF16, CBR_F16 or CBR_F32; bias float [n] or NULL; act is max(v, 0) where relu
- * is non-zero (a NaN stays one), else v.  All sums are fp32 (each matrix instruction of 128 values:
- * within 2^-23 of the sum of magnitudes), and the result is rounded once.  A scaled sum that passes fp32's
+ * is non-zero (a NaN stays one), else v.  All sums are fp32: a group of 32 is exact, each one added moves the sum
+ * by at most 2^-22 of the magnitudes so far, and the result is rounded once.  A scaled sum that passes fp32's
  * largest value within a group is an infinity, one below its smallest normal value may become 0.
  * Forward, data and weight gradient of a 1x1 convolution as for cbr_gemm_fp8.
  * m, n, k positive; m < 2^31, n, lda, ldb <= 2^22, k <= 2^23 and ceil(m / 64) * ceil(n / 64) <

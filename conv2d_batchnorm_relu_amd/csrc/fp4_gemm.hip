@@ -62,7 +62,7 @@ __device__ constexpr int apart(int p) { return ((p >> 2 ^ p >> 1) & 1) << 2 | (p
 
 // Tile kernel: 16 MS WM x 16 NS WN results a workgroup, WM x WN waves of 16 MS x 16 NS.  Both operands'
 // rows of a stage and their exponents come straight into LDS, NST stages deep, as in the 8-bit product.
-// 8192^3: 270 to 290 us, 4.1 to 3.8 PFLOP/s, with the clock down to 2 GHz by the power it takes; of it the loads alone take
+// 8192^3: 264 to 271 us, 4.2 to 4.1 PFLOP/s (the matrix instructions alone, from registers, 7.6), with the clock down to 2 GHz by the power it takes; of it the loads alone take
 // 230 us (exponents, four bytes a lane: 17), the matrix instructions 182, the reads from LDS 90.  Smaller ones are
 // bound by the way in and out of a workgroup: 50001 x 256 x 1024 17 us, of which 13 to 15 without any one of these.
 template <int BM, int BN>
@@ -318,8 +318,8 @@ struct Fp4Plan {
 // long at worst.  Tiles: a stage of 256 values takes `one` with one workgroup on a CU and `two` with two, a
 // workgroup's start and end `ends`.  Few rows: 1.2 and for each run 0.09 + 0.011 m (the more rows, the more loads), or
 // b at 4.3 TB/s; two workgroups share a CU up to 16 rows.  Joining splits takes 3 to 4 us and moves each part twice at
-// 4 TB/s.  (1 x 1000 x 2048: few rows 3.3 us, tiles of 64 5.8; 1 x 50000 x 512: 8.1, 6.0; 64 x 256 x 50176: 73 whole,
-// 14.4 in 16 splits, tiles of 64 in 48 splits 10.2.)
+// 4 TB/s.  (1 x 1000 x 2048: few rows 3.2 us, tiles of 64 5.6; 1 x 50000 x 512: 7.9, 6.0, tiles of 128 5.2; 64 x 256 x 50176:
+// few rows 73 whole, 14.5 in 14 splits, tiles of 64 67 whole, 10.8 in 28 splits (the pick), 9.9 in 40.)
 struct Costs {
     double one, two, ends;
 };

@@ -143,7 +143,8 @@ __device__ __forceinline__ void emit4(const TileArgs &p, int split, int64_t m, i
 
 // Workgroup -> tile and split.  Workgroups go to the eight XCDs in turn, each with its own L2.
 // Where k is shared out, an XCD takes whole splits (all tiles of them: the operands' columns
-// of a split are then fetched once; splits are a multiple of 8 where there are that many).
+// of a split are then fetched once) where splits are a multiple of 8.  The plans ask for one, but blocks of k that do not
+// divide leave fewer splits, and then two XCDs share some.
 // Otherwise it takes an eighth of the tiles, in groups of 8 rows of tiles walked down first,
 // so that the tiles that run together share rows of both operands.
 __device__ __forceinline__ void place(const TileArgs &p, int &tm, int &tn, int &split)

@@ -66,6 +66,12 @@ def check(layout, images, pixels, channels, groups, dtype, backward):
     assert g["chunks"] * g["ng"] >= groups > (g["chunks"] - 1) * g["ng"], what
     assert 8 * g["V"] >= g["ng"] * (channels // groups), what
     assert 4 * g["lds"] <= 160 * 1024, what
+    if backward and g["tiles"] > 1:   # the second kernel's sums
+        parts = max(1, min(g["P"] // 16, 8))
+        assert 4 * (16 * g["V"] * (parts + 1) + 2 * g["ng"]) <= 160 * 1024, what
+    last = (groups - (g["chunks"] - 1) * g["ng"]) * (channels // groups)
+    assert last >= min(8, channels), what   # a partial vector of eight is read as the chunk's last eight channels
+    assert g["tiles"] == 1 or g["V"] * g["P"] >= 64, what   # the tiles' kernels add up within whole waves
     assert offsets(g, pixels, channels, size) < 2 ** 31, what
 
 

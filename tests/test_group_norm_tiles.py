@@ -78,3 +78,22 @@ def test_far_from_zero(size):
     u = xhat * t["w"].double() + t["b"].double()
     tol = t["w"].double().abs() * (dmean * e(inv) + (x - e(mean)).abs() * e(dinv) + 5 * U * xhat.abs()) + 3 * U * (t["b"].double().abs() + u.abs())
     assert ((y.double() - u).abs() <= tol).all()
+
+
+# one image of some 2^32 bytes in tiles of up to 2^31
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", [(1, 5890, 359504, 359504), (1, 131008, 16384, 512)], ids=str)
+def test_parts_of_almost_two_to_the_31_bytes(size):
+    images, pixels, c, groups = size
+    t = dict(images=images, pixels=pixels, c=c, groups=groups, dtype="bf16", act="silu")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    t["x"], t["dy"] = (torch.empty(size[:3], dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    t["w"], t["b"] = 1 + 0.3 * torch.randn(c, generator=g, device="cuda"), 0.3 * torch.randn(c, generator=g, device="cuda")
+    y, st = G.forward(t)
+    dx, dw, db = G.backward(t, st)
+    per, many = c // groups, 2 ** 23 // pixels // (c // groups)
+    for first in (0, groups // 3, groups - many):   # some groups at a time
+        ch, gr = slice(first * per, (first + many) * per), slice(first, first + many)
+        s = {**t, "c": many * per, "groups": many, "w": t["w"][ch], "b": t["b"][ch], "x": t["x"][:, :, ch].contiguous(), "dy": t["dy"][:, :, ch].contiguous()}
+        G.check_forward(s, y[:, :, ch], st[:, gr])
+        G.check_backward(s, st[:, gr].contiguous(), dx[:, :, ch], dw[ch], db[ch])

@@ -349,8 +349,11 @@ inline int64_t workgroups(const cbr_group_norm_shape &s, const Geo &g)
     return (s.images + g.ipw - 1) / g.ipw * g.tiles * g.chunks;
 }
 inline int threads_of(const Geo &g) { return g.V * g.P * g.ipw; }
-// Outputs past the caches' 32 MB are written as streams (the next call would not find them there): 256 x 28 x 28 x 512
-// forward 92 -> 90 us, 8 x 224 x 224 x 64 fp32 backward 113 -> 98, 64 x 56 x 56 x 256 backward 109 -> 95.  Not in runs of fewer than 64 bytes, which the caches
+// Outputs past the caches' 32 MB are written as streams: 256 x 28 x 28 x 512
+// forward 92 -> 90 us, 8 x 224 x 224 x 64 fp32 backward 113 -> 98, 64 x 56 x 56 x 256 backward 109 -> 95.  With the 4-bit quantiser
+// reading the output behind it (and inputs not in the caches), large images gain as much or more (64 x 56 x 56 x 256 backward 128 ->
+// 121 us, 8 x 224 x 224 x 64 forward 57 -> 51, bf16), images held whole lose (256 x 28 x 28 x 512 forward 137 -> 146, backward 213 -> 222):
+// the 256 MB behind the L2s still hold a part of what they wrote.  Not in runs of fewer than 64 bytes, which the caches
 // have to put together (64 x 56 x 56 x 256 backward held whole, in runs of 32: 129 -> 150 us).
 inline bool streams(const cbr_group_norm_shape &s, const Geo &g)
 {

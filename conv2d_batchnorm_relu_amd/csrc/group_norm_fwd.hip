@@ -126,7 +126,8 @@ __global__ __launch_bounds__(1024) void gn_fwd_kernel(GroupNormArgs p)
 
 // First kernel of large images: each group's (mean, M2) of a tile.  A thread runs the mean and the squares about it of every
 // channel over its pixels (Welford's recurrence: eight chains side by side).  One pixel is on its way while another is
-// added: more of them cost waves (four and four, bf16: 4 x 112 x 112 x 480 48 us; one and one 34).
+// added: more of them cost waves (four and four, bf16: 4 x 112 x 112 x 480 48 us; one and one 34, both in the layout of that
+// time; the one that expected_us picks now takes 42).
 template <typename T, Tail TAIL, int NV>
 __global__ __launch_bounds__(1024) void gn_fwd_tiles_kernel(GroupNormArgs p)
 {

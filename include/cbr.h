@@ -406,8 +406,8 @@ int cbr_group_norm_forward(const cbr_group_norm_shape *shape, const void *x, con
  *   dx = (w g - sum_c w S0 / M - xhat sum_c w S1 / M) / sqrt(var + eps),
  *   dw = sum of S1 over the images,  db = sum of S0.
  * dx, dw, db may each be NULL (not wanted), not all three.  dw needs no w, db no b.  The sums run in a fixed
- * order: fp32 within an image's tile, fp64 beyond.  dx may be dy itself, or x (in place); no other
- * output may overlap an input.
+ * order, in fp32; dw and db add up the parts of images, and of large images' tiles, in fp64.  dx may be dy itself,
+ * or x (in place); no other output may overlap an input.
  */
 int cbr_group_norm_backward(const cbr_group_norm_shape *shape, const void *dy, const void *x, const float *w,
                             const float *b, const float *stats, void *dx, float *dw, float *db,
